@@ -58,6 +58,15 @@ SIGNATURES = {
     "bitlinear_linear_rows": (INT, [P, P, I64, I64, P, P, I64, P, INT, P, P]),
     "ternary_gemv_rows": (INT, [P, P, I64, I64, P, P, I64, P, P, P]),
     "bitlinear_linear_packed": (INT, [P, P, I64, I64, P, P, I64, P, INT, P, P, SZ, P]),
+    "bitlinear_optimizer_step_coef": (INT, [P, P, P, P, I64, I64, F, F, F, F, F, P, P, P, P, P, P, P, SZ, P]),
+    "bitlinear_grad_norm": (INT, [P, P, P, I64, F, P, P, P, SZ, P]),
+    "bitlinear_clip_grads": (INT, [P, P, P, P, I64, F, P, P, P, SZ, P]),
+    "bitlinear_residual_norm": (INT, [P, INT, P, INT, I64, I64, INT, P, F, INT, P, F, F, P, F, P, P, P, P, P, P, P,
+                                      P]),
+    "bitlinear_residual_norm_backward": (INT, [P, P, P, INT, P, INT, I64, I64, INT, P, P, INT, P, F, F, P, P, P, P, P,
+                                               P, P, P, SZ, P]),
+    "bitlinear_quant_weight_int8": (INT, [P, I64, I64, P, P, P, P]),
+    "bitlinear_linear_int8": (INT, [P, P, I64, I64, P, P, I64, P, INT, P, P]),
     "bitlinear_optimizer_step": (INT, [P, P, P, P, I64, I64, F, F, F, F, F, F, P, P, P, P, P, P, SZ, P]),
 }
 

@@ -23,6 +23,9 @@
 #include "rmsnorm_bwd.cuh"
 #include "gemv.cuh"
 #include "optim.cuh"
+#include "residual_norm.cuh"
+#include "grad_clip.cuh"
+#include "weight_quant8.cuh"
 #include "gemm_packed.cuh"
 #include "gemm_packed2.cuh"
 #include "mma_peak.cuh"
@@ -658,6 +661,280 @@ bl_status launch_gemv(const uint8_t* Wpacked, const float* gamma, int gamma_stri
     return launched("ternary_gemv");
 }
 
+// ------------------------------------------------------------------------------------
+// optimizer step, with its own per-matrix clip or with a given coefficient
+// ------------------------------------------------------------------------------------
+bl_status check_optimizer(const float* W, const float* dW, const float* m, const float* v, int64_t N, int64_t K,
+                          float lr, float beta1, float beta2, float eps, float weight_decay, const int32_t* step,
+                          const int8_t* Wq_i8, const uint16_t* Wq_bf16, const uint8_t* Wpacked, const float* gamma,
+                          const void* ws, size_t ws_bytes) {
+    BL_TRY(check_ptr(W, "W", true));
+    BL_TRY(check_ptr(dW, "dW", true));
+    BL_TRY(check_ptr(m, "m", true));
+    BL_TRY(check_ptr(v, "v", true));
+    BL_TRY(check_ptr(step, "step", true));
+    BL_TRY(check_ptr(gamma, "gamma", false));
+    BL_TRY(check_ptr(Wq_i8, "Wq_i8", false));
+    BL_TRY(check_ptr(Wq_bf16, "Wq_bf16", false));
+    BL_TRY(check_ptr(Wpacked, "Wpacked", false));
+    BL_TRY(check_ptr(ws, "ws", true));
+    BL_TRY(check_dims(1, N, K));
+    BL_REQUIRE(gamma != nullptr || (Wq_i8 == nullptr && Wq_bf16 == nullptr && Wpacked == nullptr), BL_ERR_INVALID_ARG,
+               "the next step's codes need gamma");
+    BL_REQUIRE(lr >= 0.0f && lr <= 1e30f, BL_ERR_INVALID_ARG, "lr must be finite and >= 0");
+    BL_REQUIRE(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f, BL_ERR_INVALID_ARG,
+               "betas must be in [0, 1)");
+    BL_REQUIRE(eps > 0.0f && eps <= 1e30f, BL_ERR_INVALID_ARG, "eps must be finite and > 0");
+    BL_REQUIRE(weight_decay >= 0.0f && weight_decay <= 1e30f, BL_ERR_INVALID_ARG,
+               "weight_decay must be finite and >= 0");
+    BL_REQUIRE(ws_bytes >= opt_ws_bytes(), BL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", opt_ws_bytes(),
+               ws_bytes);
+    return BL_OK;
+}
+
+bl::AdamwArgs adamw_args(float lr, float beta1, float beta2, float eps, float weight_decay, float max_norm) {
+    bl::AdamwArgs a{};
+    a.lr = lr;
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.eps = eps;
+    a.decay = (float)(1.0 - (double)lr * (double)weight_decay);
+    a.omb1 = (float)(1.0 - (double)beta1);
+    a.omb2 = (float)(1.0 - (double)beta2);
+    a.max_norm = max_norm;
+    return a;
+}
+
+bl_status run_optimizer(float* W, const float* dW, float* m, float* v, int64_t n, const bl::AdamwArgs& a,
+                        const float* coef, int32_t* step, int8_t* Wq_i8, uint16_t* Wq_bf16, uint8_t* Wpacked,
+                        float* gamma, void* ws, cudaStream_t st, const DeviceInfo& dev) {
+    const int parts = bl::wq_num_partials(n);
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    double* gpart = reinterpret_cast<double*>(wsb);
+    double* wpart = reinterpret_cast<double*>(wsb + kOptWpartOffset);
+    int32_t* step_next = reinterpret_cast<int32_t*>(wsb + kOptStepOffset);
+    bl::AdamwScalars* ready = nullptr;
+    if (coef != nullptr) {
+        static_assert(sizeof(bl::AdamwScalars) <= 16, "the scalars take the published step's place");
+        ready = reinterpret_cast<bl::AdamwScalars*>(wsb + kOptStepOffset);
+        pdl_launch(bl::adamw_scalars_kernel, dim3(1), dim3(32), 0, st, a, coef, step, ready);
+        BL_TRY(launched("adamw_scalars"));
+    } else {
+        pdl_launch(bl::grad_sumsq_partial_kernel, dim3(parts), dim3(bl::kWqThreads), 0, st, dW, n, gpart,
+                   static_cast<const int32_t*>(step), step_next);
+        BL_TRY(launched("grad_sumsq_partial"));
+    }
+    pdl_launch(bl::adamw_clamp_kernel, dim3(parts), dim3(bl::kWqThreads), 0, st, W, dW, m, v, n,
+               static_cast<const double*>(gpart), parts, a, static_cast<const int32_t*>(step_next), step,
+               static_cast<const bl::AdamwScalars*>(ready), gamma != nullptr ? wpart : static_cast<double*>(nullptr));
+    BL_TRY(launched("adamw_clamp"));
+    if (gamma == nullptr) return BL_OK;
+    // the next step's codes from the |W_new| partials written above (the quantiser's pass 2)
+    return run_ternary(W, n, wpart, parts, Wq_i8, Wq_bf16, Wpacked, gamma, st, dev);
+}
+
+// ------------------------------------------------------------------------------------
+// global gradient norm and clipping
+// ------------------------------------------------------------------------------------
+size_t gc_ws_bytes() { return sizeof(double) * bl::kGcMaxPartials; }
+
+bl_status check_grads(const void* const* grads, void* const* out, const int64_t* numel, const bl_dtype* dtypes,
+                      int64_t count, float max_norm, const float* norm, const float* coef, const void* ws,
+                      size_t ws_bytes) {
+    BL_REQUIRE(count >= 0 && count <= (1 << 24), BL_ERR_INVALID_ARG, "count must be in [0, 2^24], got %lld",
+               (long long)count);
+    BL_REQUIRE(count == 0 || (grads != nullptr && numel != nullptr && dtypes != nullptr), BL_ERR_INVALID_ARG,
+               "grads, numel and dtypes must not be NULL");
+    BL_REQUIRE(max_norm == max_norm && max_norm <= 1e30f, BL_ERR_INVALID_ARG, "max_norm must be finite");
+    BL_REQUIRE(norm != nullptr && coef != nullptr, BL_ERR_INVALID_ARG, "norm and coef must not be NULL");
+    BL_REQUIRE(((reinterpret_cast<uintptr_t>(norm) | reinterpret_cast<uintptr_t>(coef)) & 3u) == 0,
+               BL_ERR_MISALIGNED, "norm and coef must be 4-byte aligned");
+    BL_TRY(check_ptr(ws, "ws", true));
+    BL_REQUIRE(ws_bytes >= gc_ws_bytes(), BL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", gc_ws_bytes(),
+               ws_bytes);
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        BL_TRY(check_dtype(dtypes[i]));
+        BL_REQUIRE(numel[i] >= 0 && numel[i] <= (int64_t(1) << 40), BL_ERR_INVALID_ARG,
+                   "gradient %lld: size %lld out of range", (long long)i, (long long)numel[i]);
+        if (numel[i] == 0) continue;
+        total += numel[i];
+        BL_REQUIRE(total <= (int64_t(1) << 40), BL_ERR_UNSUPPORTED_SHAPE, "more than 2^40 elements");
+        const uintptr_t mask = dtypes[i] == BL_BF16 ? 1u : 3u;
+        BL_REQUIRE(grads[i] != nullptr && (out == nullptr || out[i] != nullptr), BL_ERR_INVALID_ARG,
+                   "gradient %lld must not be NULL", (long long)i);
+        BL_REQUIRE((reinterpret_cast<uintptr_t>(grads[i]) & mask) == 0 &&
+                       (out == nullptr || (reinterpret_cast<uintptr_t>(out[i]) & mask) == 0),
+                   BL_ERR_MISALIGNED, "gradient %lld is not aligned to its elements", (long long)i);
+    }
+    return BL_OK;
+}
+
+// Elements per chunk: four chunks a block when every block of the grid has work, between 16 KB
+// and 256 KB of fp32, so that a few large matrices and many small tensors both spread evenly.
+int64_t gc_chunk(int64_t total, int blocks) {
+    int64_t c = 4096;
+    while (c < 65536 && total / c > 4 * (int64_t)blocks) c *= 2;
+    return c;
+}
+
+// One table of the list: gradients [first, ...) as far as they fit, empty ones left out.
+// Returns the index behind the last one taken.
+template <int kMax>
+int64_t gc_fill(bl::GcTable<kMax>& tab, const void* const* grads, void* const* out, const int64_t* numel,
+                const bl_dtype* dtypes, int64_t first, int64_t count, int64_t chunk) {
+    tab.count = tab.chunks = 0;
+    tab.chunk = chunk;
+    int64_t i = first;
+    for (; i < count && tab.count < kMax; ++i) {
+        if (numel[i] == 0) continue;
+        bl::GcTensor& t = tab.t[tab.count++];
+        t.g = grads[i];
+        t.out = out != nullptr ? out[i] : nullptr;
+        t.n = numel[i];
+        t.first_chunk = tab.chunks;
+        t.bf16 = dtypes[i] == BL_BF16;
+        tab.chunks += (int32_t)((numel[i] + chunk - 1) / chunk);
+    }
+    return i;
+}
+
+template <int kMax>
+bl_status run_grads_t(const void* const* grads, void* const* out, const int64_t* numel, const bl_dtype* dtypes,
+                      int64_t count, float max_norm, float* norm, float* coef, double* partials, int blocks,
+                      int64_t chunk, cudaStream_t st) {
+    bl::GcTable<kMax> tab;
+    std::memset(&tab, 0, sizeof(tab));
+    int64_t i = 0;
+    int add = 0;
+    do {
+        i = gc_fill(tab, grads, out, numel, dtypes, i, count, chunk);
+        pdl_launch(bl::grad_sumsq_kernel<kMax>, dim3((unsigned)blocks), dim3(bl::kGcThreads), 0, st, tab, add,
+                   partials);
+        BL_TRY(launched("grad_sumsq"));
+        add = 1;
+    } while (i < count);
+    if (out == nullptr) {
+        pdl_launch(bl::grad_norm_kernel, dim3(1), dim3(bl::kGcThreads), 0, st, static_cast<const double*>(partials),
+                   blocks, max_norm, norm, coef);
+        return launched("grad_norm");
+    }
+    i = 0;
+    do {
+        i = gc_fill(tab, grads, out, numel, dtypes, i, count, chunk);
+        pdl_launch(bl::grad_scale_kernel<kMax>, dim3((unsigned)blocks), dim3(bl::kGcThreads), 0, st, tab,
+                   static_cast<const double*>(partials), blocks, max_norm, norm, coef);
+        BL_TRY(launched("grad_scale"));
+    } while (i < count);
+    return BL_OK;
+}
+
+bl_status run_grads(const void* const* grads, void* const* out, const int64_t* numel, const bl_dtype* dtypes,
+                    int64_t count, float max_norm, float* norm, float* coef, void* ws, cudaStream_t st,
+                    const DeviceInfo& dev) {
+    int64_t total = 0, full = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        total += numel[i];
+        full += numel[i] != 0;
+    }
+    const int most = std::min(4 * dev.sms, (int)bl::kGcMaxPartials);
+    const int64_t chunk = gc_chunk(total, most);
+    // no more blocks than chunks
+    const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(most, total / chunk + full));
+    double* partials = static_cast<double*>(ws);
+    if (full <= bl::kGcSmall)
+        return run_grads_t<bl::kGcSmall>(grads, out, numel, dtypes, count, max_norm, norm, coef, partials, blocks,
+                                         chunk, st);
+    return run_grads_t<bl::kGcLarge>(grads, out, numel, dtypes, count, max_norm, norm, coef, partials, blocks, chunk,
+                                     st);
+}
+
+// ------------------------------------------------------------------------------------
+// residual norms
+// ------------------------------------------------------------------------------------
+bl_status check_residual(bl_dtype x_dt, bl_dtype y_dt, int64_t T, int64_t K, int post_norm, const float* g_post,
+                         bl_gate gate_kind, const void* gate, float alpha, float beta) {
+    BL_TRY(check_dtype(x_dt));
+    BL_TRY(check_dtype(y_dt));
+    BL_REQUIRE(x_dt == BL_F32 || y_dt == BL_BF16, BL_ERR_INVALID_ARG, "a bf16 residual takes a bf16 block");
+    BL_REQUIRE(T >= 1 && K >= 1, BL_ERR_INVALID_ARG, "sizes must be positive (T=%lld K=%lld)", (long long)T,
+               (long long)K);
+    BL_REQUIRE(T <= kMaxDim, BL_ERR_UNSUPPORTED_SHAPE, "sizes must be < 2^31");
+    BL_REQUIRE(K <= kMaxRowK, BL_ERR_UNSUPPORTED_SHAPE, "K must be <= %lld for the row kernels, got %lld",
+               (long long)kMaxRowK, (long long)K);
+    BL_REQUIRE((int)gate_kind >= BL_GATE_NONE && (int)gate_kind <= BL_GATE_ELEMENT, BL_ERR_INVALID_ARG,
+               "unknown gate kind %d", (int)gate_kind);
+    BL_REQUIRE((gate != nullptr) == (gate_kind != BL_GATE_NONE), BL_ERR_INVALID_ARG,
+               "gate and gate_kind do not agree");
+    BL_TRY(check_ptr(gate, "gate", false));
+    BL_TRY(check_ptr(g_post, "g_post", false));
+    BL_REQUIRE(g_post == nullptr || post_norm, BL_ERR_INVALID_ARG, "g_post needs post_norm");
+    BL_REQUIRE(alpha - alpha == 0.0f && beta - beta == 0.0f, BL_ERR_INVALID_ARG, "alpha and beta must be finite");
+    return BL_OK;
+}
+
+size_t rn_ws_bytes(int64_t K) {
+    return sizeof(double) * bl::kRnMaxBlocks + 3 * sizeof(float) * (size_t)bl::kRnMaxBlocks * (size_t)K;
+}
+
+template <bool kBf16X, bool kBf16Y, bool kWarpRow, int E, int NT, int VPT>
+void launch_residual_norm_v(const bl::RnFwdArgs& a, cudaStream_t st) {
+    constexpr int kRows = kWarpRow ? NT / 32 : 1;
+    const dim3 grid((unsigned)((a.T + kRows - 1) / kRows));
+    if (a.gate_kind == bl::kGateElement)
+        pdl_launch(bl::residual_norm_kernel<kBf16X, kBf16Y, kWarpRow, E, NT, VPT, true>, grid, dim3(NT), 0, st, a);
+    else
+        pdl_launch(bl::residual_norm_kernel<kBf16X, kBf16Y, kWarpRow, E, NT, VPT, false>, grid, dim3(NT), 0, st, a);
+}
+
+// Rows of whole 16-byte vectors (8 elements) take the vector kernels, others one element at a
+// time; a warp per short row, a block per long one.
+template <bool kBf16X, bool kBf16Y>
+void launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st) {
+    if (a.K % 8 != 0) {
+        if (a.K <= 128) return launch_residual_norm_v<kBf16X, kBf16Y, true, 1, 256, 4>(a, st);
+        if (a.K <= 1024) return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 256, 4>(a, st);
+        if (a.K <= 4096) return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 4>(a, st);
+        return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 16>(a, st);
+    }
+    const int nvec = a.K / 8;
+    if (nvec <= 32) return launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 1>(a, st);
+    if (nvec <= 64) return launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 2>(a, st);
+    if (nvec <= 128) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 128, 1>(a, st);
+    if (nvec <= 256) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 256, 1>(a, st);
+    if (nvec <= 512) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 1>(a, st);
+    if (nvec <= 1024) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 2>(a, st);
+    launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 1024, 2>(a, st);
+}
+
+template <bool kBf16X, bool kBf16Y, int E>
+bl_status launch_residual_norm_bwd_walk(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G) {
+    constexpr int NT = 512;
+    auto kern = bl::residual_norm_bwd_walk_kernel<kBf16X, kBf16Y, E, NT>;
+    const size_t smem = 3 * sizeof(float) * (size_t)a.K;
+    static std::atomic<uint64_t> attr_set{0};   // bit d: attribute set on device d
+    int dev_id = 0;
+    cudaGetDevice(&dev_id);
+    if (!(attr_set.load() & (1ull << dev_id))) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             3 * (int)sizeof(float) * (int)kMaxRowK);
+        if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        attr_set.fetch_or(1ull << dev_id);
+    }
+    *G = (int)std::min<int64_t>(a.T, std::min(dev.sms, (int)bl::kRnMaxBlocks));
+    pdl_launch(kern, dim3((unsigned)*G), dim3(NT), smem, st, a);
+    return launched("residual_norm_bwd");
+}
+
+template <bool kBf16X, bool kBf16Y>
+bl_status launch_residual_norm_bwd(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G) {
+    if (a.K % 8 != 0) return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 1>(a, st, dev, G);
+    return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 8>(a, st, dev, G);
+}
+
+// |Xq|, |Wq| <= 128: a sum of K products stays below 2^31 for K < 2^17.
+constexpr int64_t kMaxInt8K = int64_t(1) << 17;
+
 }  // namespace
 
 // ====================================================================================
@@ -1153,56 +1430,191 @@ bl_status bitlinear_optimizer_step(float* W, const float* dW, float* m, float* v
                                    float beta1, float beta2, float eps, float weight_decay, float max_norm,
                                    int32_t* step, int8_t* Wq_i8, uint16_t* Wq_bf16, uint8_t* Wpacked, float* gamma,
                                    void* ws, size_t ws_bytes, void* stream) {
-    BL_TRY(check_ptr(W, "W", true));
-    BL_TRY(check_ptr(dW, "dW", true));
-    BL_TRY(check_ptr(m, "m", true));
-    BL_TRY(check_ptr(v, "v", true));
-    BL_TRY(check_ptr(step, "step", true));
-    BL_TRY(check_ptr(gamma, "gamma", false));
-    BL_TRY(check_ptr(Wq_i8, "Wq_i8", false));
-    BL_TRY(check_ptr(Wq_bf16, "Wq_bf16", false));
-    BL_TRY(check_ptr(Wpacked, "Wpacked", false));
-    BL_TRY(check_ptr(ws, "ws", true));
-    BL_TRY(check_dims(1, N, K));
-    BL_REQUIRE(gamma != nullptr || (Wq_i8 == nullptr && Wq_bf16 == nullptr && Wpacked == nullptr), BL_ERR_INVALID_ARG,
-               "the next step's codes need gamma");
-    BL_REQUIRE(lr >= 0.0f && lr <= 1e30f, BL_ERR_INVALID_ARG, "lr must be finite and >= 0");
-    BL_REQUIRE(beta1 >= 0.0f && beta1 < 1.0f && beta2 >= 0.0f && beta2 < 1.0f, BL_ERR_INVALID_ARG,
-               "betas must be in [0, 1)");
-    BL_REQUIRE(eps > 0.0f && eps <= 1e30f, BL_ERR_INVALID_ARG, "eps must be finite and > 0");
-    BL_REQUIRE(weight_decay >= 0.0f && weight_decay <= 1e30f, BL_ERR_INVALID_ARG,
-               "weight_decay must be finite and >= 0");
+    BL_TRY(check_optimizer(W, dW, m, v, N, K, lr, beta1, beta2, eps, weight_decay, step, Wq_i8, Wq_bf16, Wpacked,
+                           gamma, ws, ws_bytes));
     BL_REQUIRE(max_norm == max_norm && max_norm <= 1e30f, BL_ERR_INVALID_ARG, "max_norm must be finite");
-    BL_REQUIRE(ws_bytes >= opt_ws_bytes(), BL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", opt_ws_bytes(),
-               ws_bytes);
     DeviceInfo dev;
     BL_TRY(current_device(&dev));
+    return run_optimizer(W, dW, m, v, N * K, adamw_args(lr, beta1, beta2, eps, weight_decay, max_norm), nullptr, step,
+                         Wq_i8, Wq_bf16, Wpacked, gamma, ws, static_cast<cudaStream_t>(stream), dev);
+}
+
+bl_status bitlinear_optimizer_step_coef(float* W, const float* dW, float* m, float* v, int64_t N, int64_t K,
+                                        float lr, float beta1, float beta2, float eps, float weight_decay,
+                                        const float* coef, int32_t* step, int8_t* Wq_i8, uint16_t* Wq_bf16,
+                                        uint8_t* Wpacked, float* gamma, void* ws, size_t ws_bytes, void* stream) {
+    BL_TRY(check_optimizer(W, dW, m, v, N, K, lr, beta1, beta2, eps, weight_decay, step, Wq_i8, Wq_bf16, Wpacked,
+                           gamma, ws, ws_bytes));
+    BL_REQUIRE(coef != nullptr, BL_ERR_INVALID_ARG, "coef must not be NULL");
+    BL_REQUIRE((reinterpret_cast<uintptr_t>(coef) & 3u) == 0, BL_ERR_MISALIGNED, "coef must be 4-byte aligned");
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    return run_optimizer(W, dW, m, v, N * K, adamw_args(lr, beta1, beta2, eps, weight_decay, 0.0f), coef, step, Wq_i8,
+                         Wq_bf16, Wpacked, gamma, ws, static_cast<cudaStream_t>(stream), dev);
+}
+
+// ------------------------------------------------------------------------------------
+// global gradient norm and clipping
+// ------------------------------------------------------------------------------------
+bl_status bitlinear_grad_norm(const void* const* grads, const int64_t* numel, const bl_dtype* dtypes, int64_t count,
+                              float max_norm, float* norm, float* coef, void* ws, size_t ws_bytes, void* stream) {
+    BL_TRY(check_grads(grads, nullptr, numel, dtypes, count, max_norm, norm, coef, ws, ws_bytes));
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    return run_grads(grads, nullptr, numel, dtypes, count, max_norm, norm, coef, ws, static_cast<cudaStream_t>(stream),
+                     dev);
+}
+
+bl_status bitlinear_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
+                               const bl_dtype* dtypes, int64_t count, float max_norm, float* norm, float* coef,
+                               void* ws, size_t ws_bytes, void* stream) {
+    BL_REQUIRE(out != nullptr, BL_ERR_INVALID_ARG, "out must not be NULL");
+    BL_TRY(check_grads(grads, out, numel, dtypes, count, max_norm, norm, coef, ws, ws_bytes));
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    return run_grads(grads, out, numel, dtypes, count, max_norm, norm, coef, ws, static_cast<cudaStream_t>(stream),
+                     dev);
+}
+
+// ------------------------------------------------------------------------------------
+// residual norms
+// ------------------------------------------------------------------------------------
+bl_status bitlinear_residual_norm(const void* X, bl_dtype x_dt, const void* Y, bl_dtype y_dt, int64_t T, int64_t K,
+                                  int post_norm, const float* g_post, float eps_post, bl_gate gate_kind,
+                                  const void* gate, float alpha, float beta, const float* g_pre, float eps_pre,
+                                  void* Xout, float* r_post, float* r_pre, void* H, int8_t* Xq, float* sx, void* Xdq,
+                                  void* stream) {
+    BL_TRY(check_residual(x_dt, y_dt, T, K, post_norm, g_post, gate_kind, gate, alpha, beta));
+    BL_TRY(check_ptr(X, "X", true));
+    BL_TRY(check_ptr(Y, "Y", true));
+    BL_TRY(check_ptr(Xout, "Xout", true));
+    BL_TRY(check_ptr(r_post, "r_post", post_norm != 0));
+    BL_TRY(check_ptr(g_pre, "g_pre", false));
+    BL_TRY(check_ptr(H, "H", false));
+    BL_TRY(check_ptr(Xq, "Xq", false));
+    BL_TRY(check_ptr(sx, "sx", Xq != nullptr));
+    BL_TRY(check_ptr(Xdq, "Xdq", false));
+    BL_TRY(check_ptr(r_pre, "r_pre", H != nullptr || Xq != nullptr));
+    BL_REQUIRE(H == nullptr || Xq == nullptr, BL_ERR_INVALID_ARG, "H and Xq exclude each other");
+    BL_REQUIRE(Xq != nullptr || Xdq == nullptr, BL_ERR_INVALID_ARG, "Xdq needs Xq");
+    BL_REQUIRE(H != nullptr || Xq != nullptr || g_pre == nullptr, BL_ERR_INVALID_ARG, "g_pre needs H or Xq");
+    BL_REQUIRE(eps_post >= 0.0f && eps_post <= 1e30f && eps_pre >= 0.0f && eps_pre <= 1e30f, BL_ERR_INVALID_ARG,
+               "eps must be finite and >= 0");
+    BL_REQUIRE(Xq == nullptr || K % 32 == 0, BL_ERR_UNSUPPORTED_SHAPE,
+               "the quantised output needs K to be a multiple of 32, got %lld", (long long)K);
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    bl::RnFwdArgs a{};
+    a.x = X; a.y = Y; a.gate = gate; a.g_post = g_post; a.g_pre = g_pre;
+    a.xout = Xout; a.r_post = r_post; a.r_pre = (H != nullptr || Xq != nullptr) ? r_pre : nullptr;
+    a.h = H; a.xq = Xq; a.sx = sx; a.xdq = Xdq;
+    a.T = (int)T; a.K = (int)K;
+    a.post = post_norm != 0; a.gate_kind = (int)gate_kind;
+    a.alpha = alpha; a.beta = beta; a.eps_post = eps_post; a.eps_pre = eps_pre;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int64_t n = N * K;
-    const int parts = bl::wq_num_partials(n);
-    uint8_t* wsb = static_cast<uint8_t*>(ws);
-    double* gpart = reinterpret_cast<double*>(wsb);
-    double* wpart = reinterpret_cast<double*>(wsb + kOptWpartOffset);
-    int32_t* step_next = reinterpret_cast<int32_t*>(wsb + kOptStepOffset);
-    bl::AdamwArgs a{};
-    a.lr = lr;
-    a.beta1 = beta1;
-    a.beta2 = beta2;
-    a.eps = eps;
-    a.decay = (float)(1.0 - (double)lr * (double)weight_decay);
-    a.omb1 = (float)(1.0 - (double)beta1);
-    a.omb2 = (float)(1.0 - (double)beta2);
-    a.max_norm = max_norm;
-    pdl_launch(bl::grad_sumsq_partial_kernel, dim3(parts), dim3(bl::kWqThreads), 0, st, dW, n, gpart,
-               static_cast<const int32_t*>(step), step_next);
-    BL_TRY(launched("grad_sumsq_partial"));
-    pdl_launch(bl::adamw_clamp_kernel, dim3(parts), dim3(bl::kWqThreads), 0, st, W, dW, m, v, n,
-               static_cast<const double*>(gpart), parts, a, static_cast<const int32_t*>(step_next), step,
-               gamma != nullptr ? wpart : static_cast<double*>(nullptr));
-    BL_TRY(launched("adamw_clamp"));
-    if (gamma == nullptr) return BL_OK;
-    // the next step's codes from the |W_new| partials written above (the quantiser's pass 2)
-    return run_ternary(W, n, wpart, parts, Wq_i8, Wq_bf16, Wpacked, gamma, st, dev);
+    if (x_dt == BL_BF16) launch_residual_norm<true, true>(a, st);
+    else if (y_dt == BL_BF16) launch_residual_norm<false, true>(a, st);
+    else launch_residual_norm<false, false>(a, st);
+    return launched("residual_norm");
+}
+
+bl_status bitlinear_residual_norm_backward(const float* dXout, const float* dH, const void* Xout, bl_dtype x_dt,
+                                           const void* Y, bl_dtype y_dt, int64_t T, int64_t K, int post_norm,
+                                           const float* g_post, const float* r_post, bl_gate gate_kind,
+                                           const void* gate, float alpha, float beta, const float* g_pre,
+                                           const float* r_pre, float* dX, void* dY, float* dg_post, float* dg_pre,
+                                           void* dgate, void* ws, size_t ws_bytes, void* stream) {
+    BL_TRY(check_residual(x_dt, y_dt, T, K, post_norm, g_post, gate_kind, gate, alpha, beta));
+    BL_TRY(check_ptr(dXout, "dXout", false));
+    BL_TRY(check_ptr(dH, "dH", false));
+    BL_REQUIRE(dXout != nullptr || dH != nullptr, BL_ERR_INVALID_ARG, "dXout and dH must not both be NULL");
+    BL_TRY(check_ptr(Xout, "Xout", dH != nullptr));
+    BL_TRY(check_ptr(Y, "Y", true));
+    BL_TRY(check_ptr(r_post, "r_post", post_norm != 0));
+    BL_TRY(check_ptr(r_pre, "r_pre", dH != nullptr));
+    BL_TRY(check_ptr(g_pre, "g_pre", false));
+    BL_TRY(check_ptr(dX, "dX", true));
+    BL_TRY(check_ptr(dY, "dY", true));
+    BL_TRY(check_ptr(dg_post, "dg_post", false));
+    BL_TRY(check_ptr(dg_pre, "dg_pre", false));
+    BL_TRY(check_ptr(dgate, "dgate", false));
+    BL_REQUIRE(dg_post == nullptr || post_norm, BL_ERR_INVALID_ARG, "dg_post needs post_norm");
+    BL_REQUIRE(dg_pre == nullptr || dH != nullptr, BL_ERR_INVALID_ARG, "dg_pre needs dH");
+    BL_REQUIRE(dgate == nullptr || gate_kind != BL_GATE_NONE, BL_ERR_INVALID_ARG, "dgate needs a gate");
+    const bool sums = dg_post != nullptr || dg_pre != nullptr ||
+                      (dgate != nullptr && (gate_kind == BL_GATE_SCALAR || gate_kind == BL_GATE_CHANNEL));
+    BL_TRY(check_ptr(ws, "ws", sums));
+    BL_REQUIRE(!sums || ws_bytes >= rn_ws_bytes(K), BL_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu",
+               rn_ws_bytes(K), ws_bytes);
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    bl::RnBwdArgs a{};
+    a.dx = dXout; a.dh = dH; a.x = Xout; a.y = Y; a.gate = gate;
+    a.r_post = r_post; a.r_pre = r_pre; a.g_post = g_post; a.g_pre = g_pre;
+    a.dX = dX; a.dY = dY;
+    a.T = (int)T; a.K = (int)K;
+    a.post = post_norm != 0; a.gate_kind = (int)gate_kind;
+    a.alpha = alpha; a.beta = beta;
+    // the scalar's partials first (fp64), then one [blocks x K] array for each column sum
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    float* part = reinterpret_cast<float*>(w + sizeof(double) * bl::kRnMaxBlocks);
+    const int64_t rows = bl::kRnMaxBlocks * K;
+    if (dg_pre != nullptr) a.part_pre = part;
+    if (dg_post != nullptr) a.part_post = part + rows;
+    if (dgate != nullptr) {
+        if (gate_kind == BL_GATE_CHANNEL) a.part_gate = part + 2 * rows;
+        else if (gate_kind == BL_GATE_SCALAR) a.part_scalar = reinterpret_cast<double*>(w);
+        else a.dgate = dgate;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int G = 0;
+    if (x_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<true, true>(a, st, dev, &G)));
+    else if (y_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<false, true>(a, st, dev, &G)));
+    else BL_TRY((launch_residual_norm_bwd<false, false>(a, st, dev, &G)));
+    if (!sums) return BL_OK;
+    bl::RnReduceArgs r{};
+    r.part[0] = a.part_pre; r.part[1] = a.part_post; r.part[2] = a.part_gate;
+    r.out[0] = dg_pre; r.out[1] = dg_post; r.out[2] = static_cast<float*>(dgate);
+    r.part_scalar = a.part_scalar; r.dscalar = static_cast<float*>(dgate);
+    r.G = G; r.K = (int)K;
+    pdl_launch(bl::rn_reduce_kernel, dim3((unsigned)((K + 31) / 32), 3), dim3(1024), 0, st, r);
+    return launched("residual_norm_reduce");
+}
+
+// ------------------------------------------------------------------------------------
+// 8-bit linear
+// ------------------------------------------------------------------------------------
+bl_status bitlinear_quant_weight_int8(const float* W, int64_t N, int64_t K, int8_t* Wq_i8, uint16_t* Wq_bf16,
+                                      float* gamma_rows, void* stream) {
+    BL_TRY(check_ptr(W, "W", true));
+    BL_TRY(check_ptr(gamma_rows, "gamma_rows", true));
+    BL_TRY(check_ptr(Wq_i8, "Wq_i8", false));
+    BL_TRY(check_ptr(Wq_bf16, "Wq_bf16", false));
+    BL_TRY(check_dims(1, N, K));
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    pdl_launch(bl::weight_quant8_kernel, dim3((unsigned)N), dim3(bl::kW8Threads), 0,
+               static_cast<cudaStream_t>(stream), W, (int)N, (int)K, Wq_i8, Wq_bf16, gamma_rows);
+    return launched("weight_quant8");
+}
+
+bl_status bitlinear_linear_int8(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq_i8,
+                                const float* gamma_rows, int64_t N, void* Y, bl_dtype y_dt, int32_t* acc,
+                                void* stream) {
+    BL_TRY(check_dtype(y_dt));
+    BL_TRY(check_ptr(Xq, "Xq", true));
+    BL_TRY(check_ptr(sx, "sx", true));
+    BL_TRY(check_ptr(Wq_i8, "Wq_i8", true));
+    BL_TRY(check_ptr(gamma_rows, "gamma_rows", true));
+    BL_TRY(check_ptr(Y, "Y", true));
+    BL_TRY(check_ptr(acc, "acc", false));
+    BL_TRY(check_dims(T, N, K));
+    BL_REQUIRE(K < kMaxInt8K, BL_ERR_UNSUPPORTED_SHAPE,
+               "K must be below %lld: 128 * 128 * K has to fit the int32 accumulator, got %lld", (long long)kMaxInt8K,
+               (long long)K);
+    DeviceInfo dev;
+    BL_TRY(current_device(&dev));
+    return run_linear_rows(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, y_dt, acc, static_cast<cudaStream_t>(stream), dev);
 }
 
 bl_status bl_mma_peak_probe(int kind, int pair, int iters, double* ops_out, void* stream) {

@@ -79,6 +79,30 @@ struct AdamwScalars {
     float bc2_sqrt;    // sqrt(1 - beta2^t)
 };
 
+// Scalars of step t with clip coefficient c (fp64, rounded once).
+__device__ __forceinline__ AdamwScalars adamw_scalars(const AdamwArgs& a, double c, double t) {
+    const double bc1 = 1.0 - pow(static_cast<double>(a.beta1), t);
+    const double bc2 = 1.0 - pow(static_cast<double>(a.beta2), t);
+    AdamwScalars sc;
+    sc.c = static_cast<float>(c);
+    sc.step_size = static_cast<float>(static_cast<double>(a.lr) / bc1);
+    sc.bc2_sqrt = static_cast<float>(sqrt(bc2));
+    return sc;
+}
+
+// The step with a given clip coefficient (the global norm's) needs no pass over dW of its own:
+// one thread advances the step index and forms the scalars for the update that follows.
+__global__ void __launch_bounds__(32) adamw_scalars_kernel(AdamwArgs a, const float* __restrict__ coef,
+                                                           int32_t* __restrict__ step,
+                                                           AdamwScalars* __restrict__ ready) {
+    pdl_trigger_and_wait();
+    if (threadIdx.x == 0) {
+        const int32_t t = *step + 1;
+        *step = t;
+        *ready = adamw_scalars(a, static_cast<double>(*coef), static_cast<double>(t));
+    }
+}
+
 __device__ __forceinline__ float adamw_elem(float w, float dw, float& m, float& v, const AdamwArgs& a,
                                             const AdamwScalars& s) {
     const float g = __fmul_rn(s.c, dw);
@@ -90,15 +114,16 @@ __device__ __forceinline__ float adamw_elem(float w, float dw, float& m, float& 
 }
 
 // Grid = the partial count of the weight quantiser's pass 1 for n (wq_num_partials), so
-// block b visits exactly the vectors that pass 1's block b would, in the same order.
+// block b visits exactly the vectors that pass 1's block b would, in the same order.  With
+// `ready` the scalars are there already (adamw_scalars_kernel); gpart and the steps are unused.
 __global__ void __launch_bounds__(kWqThreads) adamw_clamp_kernel(
     float* __restrict__ W, const float* __restrict__ dW, float* __restrict__ m, float* __restrict__ v, int64_t n,
     const double* __restrict__ gpart, int nparts, AdamwArgs a, const int32_t* __restrict__ step_next,
-    int32_t* __restrict__ step, double* __restrict__ wpart) {
+    int32_t* __restrict__ step, const AdamwScalars* __restrict__ ready, double* __restrict__ wpart) {
     __shared__ double red[kWqThreads / 32];
     __shared__ AdamwScalars s_sc;
     pdl_trigger_and_wait();
-    {
+    if (ready == nullptr) {
         // fixed-order sum of the dW^2 partials (as the quantiser's pass 2 sums its partials)
         constexpr int kPerThread = (kWqMaxPartials + kWqThreads - 1) / kWqThreads;
         double acc = 0.0;
@@ -119,19 +144,12 @@ __global__ void __launch_bounds__(kWqThreads) adamw_clamp_kernel(
                 c = static_cast<double>(a.max_norm) / (sqrt(S) + 1e-6);
                 if (c > 1.0) c = 1.0;
             }
-            const double t = static_cast<double>(*step_next);
-            const double bc1 = 1.0 - pow(static_cast<double>(a.beta1), t);
-            const double bc2 = 1.0 - pow(static_cast<double>(a.beta2), t);
-            AdamwScalars sc;
-            sc.c = static_cast<float>(c);
-            sc.step_size = static_cast<float>(static_cast<double>(a.lr) / bc1);
-            sc.bc2_sqrt = static_cast<float>(sqrt(bc2));
-            s_sc = sc;
+            s_sc = adamw_scalars(a, c, static_cast<double>(*step_next));
             if (blockIdx.x == 0) *step = *step_next;
         }
         __syncthreads();
     }
-    const AdamwScalars sc = s_sc;
+    const AdamwScalars sc = ready == nullptr ? s_sc : *ready;
     const int64_t nvec = n / 4;
     float4* w4 = reinterpret_cast<float4*>(W);
     const float4* g4 = reinterpret_cast<const float4*>(dW);

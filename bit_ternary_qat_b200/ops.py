@@ -40,6 +40,23 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _same(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
+    """Address of a contiguous tensor of this type, shape and device; raises if it is another."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+    return t.data_ptr()
+
+
+def _call(dev, name: str, *args) -> None:
+    """Call an entry point on the current stream of the tensors' device, that device current."""
+    if torch.cuda.current_device() == dev.index:
+        _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+
+
 def workspace_bytes(T: int, N: int, K: int) -> int:
     return int(_lib.lib().bitlinear_workspace_bytes(T, N, K))
 
@@ -415,9 +432,12 @@ def ternary_gemv_rows(packed: torch.Tensor, gamma_rows: torch.Tensor, K: int, xq
 def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor, v: torch.Tensor,
                              step: torch.Tensor, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-6,
                              weight_decay: float = 0.01, max_norm: float = 1.0, requantize: bool = False,
-                             ws: Optional[torch.Tensor] = None, out=None):
+                             ws: Optional[torch.Tensor] = None, out=None,
+                             coef: Optional[torch.Tensor] = None):
     """Updates W, m, v (fp32) and step (int32 [1]) in place.  With requantize, returns
-    dict(gamma, wq_i8, wq_bf16, packed) of the updated W (keys from ``out`` are reused)."""
+    dict(gamma, wq_i8, wq_bf16, packed) of the updated W (keys from ``out`` are reused).
+    coef (fp32 [1], bitlinear_grad_norm's) takes the place of the per-matrix clip: dW is scaled
+    by it and max_norm is not used."""
     for t, name in ((W, "W"), (dW, "dW"), (m, "m"), (v, "v")):
         _cuda(t, name, torch.float32)
     _cuda(step, "step", torch.int32)
@@ -431,11 +451,242 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
         o.setdefault("packed", torch.empty(N, K // 4, dtype=torch.uint8, device=dev))
     if ws is None:
         ws = workspace(1, N, K, dev)
+    if coef is not None:
+        _same(dW, "dW", torch.float32, W.shape, dev)
+        _same(m, "m", torch.float32, W.shape, dev)
+        _same(v, "v", torch.float32, W.shape, dev)
+        _same(step, "step", torch.int32, (1,), dev)
+        _same(coef, "coef", torch.float32, (1,), dev)
+        _call(dev, "bitlinear_optimizer_step_coef", W.data_ptr(), dW.data_ptr(), m.data_ptr(), v.data_ptr(), N, K,
+              lr, betas[0], betas[1], eps, weight_decay, coef.data_ptr(), step.data_ptr(), _ptr(o.get("wq_i8")),
+              _ptr(o.get("wq_bf16")), _ptr(o.get("packed")), _ptr(o.get("gamma")), ws.data_ptr(), ws.numel())
+        return o
     _lib.call("bitlinear_optimizer_step", W.data_ptr(), dW.data_ptr(), m.data_ptr(), v.data_ptr(), N, K,
               float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay), float(max_norm),
               step.data_ptr(), _ptr(o.get("wq_i8")), _ptr(o.get("wq_bf16")), _ptr(o.get("packed")),
               _ptr(o.get("gamma")), ws.data_ptr(), ws.numel(), _stream(dev))
     return o
+
+
+# ----------------------------------------------------------------------------------
+# global gradient norm and clipping
+# ----------------------------------------------------------------------------------
+
+def _grad_lists(grads, out):
+    """Device, and the host arrays that the entry points take: addresses, counts, types."""
+    n = len(grads)
+    if n == 0:
+        raise ValueError("grads must not be empty")
+    dev = grads[0].device
+    if out is not None and len(out) != n:
+        raise ValueError(f"out must have {n} tensors, got {len(out)}")
+    for i, g in enumerate(grads):
+        if g.device != dev or not g.is_cuda:
+            raise ValueError(f"grads[{i}] must be a CUDA tensor on {dev}, got {g.device}")
+        if g.dtype not in _DT:
+            raise ValueError(f"grads[{i}]: unsupported dtype {g.dtype}")
+        if not g.is_contiguous():
+            raise ValueError(f"grads[{i}] must be contiguous")
+        if out is not None:
+            _same(out[i], f"out[{i}]", g.dtype, g.shape, dev)
+    ptrs = (_lib.P * n)(*[g.data_ptr() for g in grads])
+    outs = (_lib.P * n)(*[t.data_ptr() for t in out]) if out is not None else ptrs
+    return dev, ptrs, outs, (_lib.I64 * n)(*[g.numel() for g in grads]), (_lib.INT * n)(*[_DT[g.dtype] for g in grads])
+
+
+def _norm_outputs(dev, norm, coef, ws):
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+    if coef is None:
+        coef = torch.empty(1, dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = workspace(1, 1, 1, dev)
+    _same(norm, "norm", torch.float32, (1,), dev)
+    _same(coef, "coef", torch.float32, (1,), dev)
+    return norm, coef, ws
+
+
+def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tensor] = None,
+                        coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Global L2 norm of a list of gradients (fp32 or bf16, any shapes) and its clip coefficient.
+    Returns dict(norm [1] f32, coef [1] f32); coef goes into bitlinear_optimizer_step."""
+    dev, ptrs, _, numel, types = _grad_lists(grads, None)
+    norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
+    _call(dev, "bitlinear_grad_norm", ptrs, numel, types, len(grads), max_norm, norm.data_ptr(), coef.data_ptr(),
+          ws.data_ptr(), ws.numel() * ws.element_size())
+    return {"norm": norm, "coef": coef}
+
+
+def bitlinear_clip_grads(grads, max_norm: float = 1.0, out=None, norm: Optional[torch.Tensor] = None,
+                         coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Scales a list of gradients by the clip coefficient of their global norm, in place or into
+    ``out``.  Returns dict(norm [1] f32, coef [1] f32, grads: the scaled list)."""
+    dev, ptrs, outs, numel, types = _grad_lists(grads, out)
+    if len({p for p, n in zip(outs, numel) if n}) != sum(1 for n in numel if n):
+        raise ValueError("a gradient is written twice")
+    norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
+    _call(dev, "bitlinear_clip_grads", ptrs, outs, numel, types, len(grads), max_norm, norm.data_ptr(),
+          coef.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
+    return {"norm": norm, "coef": coef, "grads": grads if out is None else out}
+
+
+# ----------------------------------------------------------------------------------
+# residual norms: between two BitLinears
+# ----------------------------------------------------------------------------------
+
+GATE_NONE, GATE_SCALAR, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(5)
+
+
+def _gate(gate: Optional[torch.Tensor], T: int, K: int, y_dtype, dev):
+    """(gate kind, address): [1] scalar, [K] channel, [T, 1] token (fp32), [T, K] element (y's type)."""
+    if gate is None:
+        return GATE_NONE, None
+    if gate.dim() == 2 and gate.shape[1] == 1 and (K != 1 or gate.dtype is torch.float32):
+        return GATE_TOKEN, _same(gate, "gate", torch.float32, (T, 1), dev)
+    if gate.dim() == 2:
+        return GATE_ELEMENT, _same(gate, "gate", y_dtype, (T, K), dev)
+    if gate.dim() == 1 and gate.shape[0] == 1:
+        return GATE_SCALAR, _same(gate, "gate", torch.float32, (1,), dev)
+    return GATE_CHANNEL, _same(gate, "gate", torch.float32, (K,), dev)
+
+
+def _residual_types(x: torch.Tensor, y: torch.Tensor):
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError("x must be a CUDA tensor [T, K]")
+    if (x.dtype, y.dtype) not in ((torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
+                                  (torch.float32, torch.bfloat16)):
+        raise ValueError(f"unsupported types: residual {x.dtype}, block {y.dtype}")
+    return x.shape, x.device
+
+
+def bitlinear_residual_norm(x: torch.Tensor, y: torch.Tensor, post_norm: bool = True,
+                            g_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                            alpha: float = 1.0, beta: float = 1.0, mode: str = "quant",
+                            g_pre: Optional[torch.Tensor] = None, eps_post: float = 1e-6, eps_pre: float = 1e-6,
+                            want_xdq: bool = True, out=None):
+    """From a block's output y to the next block's operand: x' = alpha x + beta gate norm(y), then
+    the norm of x' quantised (mode "quant": the operand of bitlinear_linear*), as it is ("norm")
+    or not taken ("none").  gate: None, [1], [K] or [T, 1] fp32, or [T, K] of y's type.
+    Returns dict(x [T,K] of x's type, r_post [T] f32 with post_norm, and by mode: r_pre [T] f32,
+    xq [T,K] i8, sx [T] f32, xdq [T,K] of y's type; or r_pre, h [T,K] of y's type).
+    out["x"] may be x itself."""
+    shape, dev = _residual_types(x, y)
+    T, K = shape
+    o = {} if out is None else dict(out)
+    row, f32 = (T,), torch.float32
+
+    def buf(name, sh, dtype):
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(sh, dtype=dtype, device=dev)
+            return t.data_ptr()
+        return _same(t, name, dtype, sh, dev)
+
+    px, py = _same(x, "x", x.dtype, shape, dev), _same(y, "y", y.dtype, shape, dev)
+    kind, pgate = _gate(gate, T, K, y.dtype, dev)
+    r_post = r_pre = h = xq = sx = xdq = None
+    if post_norm:
+        r_post = buf("r_post", row, f32)
+    if mode == "quant":
+        r_pre, xq, sx = buf("r_pre", row, f32), buf("xq", shape, torch.int8), buf("sx", row, f32)
+        if want_xdq:
+            xdq = buf("xdq", shape, y.dtype)
+    elif mode == "norm":
+        r_pre, h = buf("r_pre", row, f32), buf("h", shape, y.dtype)
+    elif mode != "none":
+        raise ValueError(f"mode must be 'quant', 'norm' or 'none', got {mode!r}")
+    _call(dev, "bitlinear_residual_norm", px, _DT[x.dtype], py, _DT[y.dtype], T, K, 1 if post_norm else 0,
+          None if g_post is None else _same(g_post, "g_post", f32, (K,), dev), eps_post, kind, pgate, alpha, beta,
+          None if g_pre is None else _same(g_pre, "g_pre", f32, (K,), dev), eps_pre, buf("x", shape, x.dtype), r_post,
+          r_pre, h, xq, sx, xdq)
+    return o
+
+
+def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: torch.Tensor,
+                                     y: torch.Tensor, r_post: Optional[torch.Tensor] = None,
+                                     r_pre: Optional[torch.Tensor] = None, g_post: Optional[torch.Tensor] = None,
+                                     gate: Optional[torch.Tensor] = None, alpha: float = 1.0, beta: float = 1.0,
+                                     g_pre: Optional[torch.Tensor] = None, want_dgains: bool = True,
+                                     want_dgate: bool = True, ws: Optional[torch.Tensor] = None, out=None):
+    """Gradient of bitlinear_residual_norm.  dx [T,K] f32: gradient of the new residual from past
+    the next block (or None); dh [T,K] f32: gradient of the norm output, bitlinear_grad_input's
+    result (or None: mode "none").  x: the forward's NEW residual; r_post (None: no post norm),
+    r_pre: its saved statistics.  Returns dict(dx [T,K] f32, dy [T,K] of y's type, and with
+    want_dgains / want_dgate: dpost_gain [K], dpre_gain [K] f32 (with the norm in question),
+    dgate as the gate).  out["dx"] may be dx or dh."""
+    shape, dev = _residual_types(x, y)
+    T, K = shape
+    o = {} if out is None else dict(out)
+    f32 = torch.float32
+
+    def buf(name, sh, dtype):
+        t = o.get(name)
+        if t is None:
+            t = o[name] = torch.empty(sh, dtype=dtype, device=dev)
+            return t.data_ptr()
+        return _same(t, name, dtype, sh, dev)
+
+    def opt(t, name, sh):
+        return None if t is None else _same(t, name, f32, sh, dev)
+
+    if dh is not None and r_pre is None:
+        raise ValueError("dh needs r_pre")
+    kind, pgate = _gate(gate, T, K, y.dtype, dev)
+    dg_post = buf("dpost_gain", (K,), f32) if want_dgains and r_post is not None else None
+    dg_pre = buf("dpre_gain", (K,), f32) if want_dgains and dh is not None else None
+    dgate = buf("dgate", gate.shape, gate.dtype) if want_dgate and gate is not None else None
+    if ws is None and (dg_post is not None or dg_pre is not None or
+                       (dgate is not None and kind in (GATE_SCALAR, GATE_CHANNEL))):
+        ws = workspace(T, 16, K, dev)
+    _call(dev, "bitlinear_residual_norm_backward", opt(dx, "dx", shape), opt(dh, "dh", shape),
+          _same(x, "x", x.dtype, shape, dev), _DT[x.dtype], _same(y, "y", y.dtype, shape, dev), _DT[y.dtype], T, K,
+          0 if r_post is None else 1, opt(g_post, "g_post", (K,)), opt(r_post, "r_post", (T,)), kind, pgate, alpha,
+          beta, opt(g_pre, "g_pre", (K,)), opt(r_pre, "r_pre", (T,)), buf("dx", shape, f32), buf("dy", shape, y.dtype),
+          dg_post, dg_pre, dgate, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    return o
+
+
+# ----------------------------------------------------------------------------------
+# 8-bit linear: a scale for each token and each channel
+# ----------------------------------------------------------------------------------
+
+def bitlinear_quant_weight_int8(W: torch.Tensor, want_i8: bool = True, want_bf16: bool = True, out=None):
+    """8-bit codes of the rows of W [N,K] f32.  Returns dict(gamma_rows [N] f32, wq_i8 [N,K] i8,
+    wq_bf16 [N,K] bf16 (= W_q * bf16(gamma_n), the backward's operand with a gamma of 1))."""
+    _cuda(W, "W", torch.float32)
+    N, K = W.shape
+    dev = W.device
+    o = {} if out is None else dict(out)
+    for name, shape, dtype, want in (("gamma_rows", (N,), torch.float32, True), ("wq_i8", (N, K), torch.int8, want_i8),
+                                     ("wq_bf16", (N, K), torch.bfloat16, want_bf16)):
+        if name in o:
+            _same(o[name], name, dtype, shape, dev)
+        elif want:
+            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+    _call(dev, "bitlinear_quant_weight_int8", W.data_ptr(), N, K, _ptr(o.get("wq_i8")), _ptr(o.get("wq_bf16")),
+          o["gamma_rows"].data_ptr())
+    return o
+
+
+def bitlinear_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tensor, gamma_rows: torch.Tensor,
+                          out_dtype=torch.bfloat16, want_acc: bool = False, y: Optional[torch.Tensor] = None,
+                          acc: Optional[torch.Tensor] = None):
+    """y[t,n] = acc[t,n] * (gamma_rows[n] / sx[t]) from 8-bit codes, one token to many.  Returns
+    (y [T,N], acc [T,N] i32 or None)."""
+    if not xq.is_cuda:
+        raise ValueError("xq must be a CUDA tensor")
+    dev = xq.device
+    T, K = xq.shape
+    N = wq_i8.shape[0]
+    if y is None:
+        y = torch.empty(T, N, dtype=out_dtype, device=dev)
+    if want_acc and acc is None:
+        acc = torch.empty(T, N, dtype=torch.int32, device=dev)
+    _call(dev, "bitlinear_linear_int8", _same(xq, "xq", torch.int8, (T, K), dev),
+          _same(sx, "sx", torch.float32, (T,), dev), T, K, _same(wq_i8, "wq_i8", torch.int8, (N, K), dev),
+          _same(gamma_rows, "gamma_rows", torch.float32, (N,), dev), N, _same(y, "y", y.dtype, (T, N), dev), _dt(y),
+          None if acc is None else _same(acc, "acc", torch.int32, (T, N), dev))
+    return y, acc
 
 
 def check_device_status(device=None) -> int:

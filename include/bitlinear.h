@@ -68,6 +68,12 @@ typedef enum {
 
 typedef enum { BL_F32 = 0, BL_BF16 = 1 } bl_dtype;
 
+/* What a gate is given for: nothing, the whole tensor ([1]), each channel ([K]), each token
+ * ([T]) or each element ([T x K]). */
+typedef enum {
+    BL_GATE_NONE = 0, BL_GATE_SCALAR = 1, BL_GATE_CHANNEL = 2, BL_GATE_TOKEN = 3, BL_GATE_ELEMENT = 4
+} bl_gate;
+
 /* ABI version of this header (bumped on any signature change). */
 #define BITLINEAR_ABI_VERSION 1
 BL_API int bl_abi_version(void);
@@ -351,6 +357,105 @@ BL_API bl_status bitlinear_optimizer_step(float* W, const float* dW, float* m, f
                                    float eps, float weight_decay, float max_norm, int32_t* step,
                                    int8_t* Wq_i8, uint16_t* Wq_bf16, uint8_t* Wpacked,
                                    float* gamma, void* ws, size_t ws_bytes, void* stream);
+
+/* The same step with a clip coefficient that is there already (bitlinear_grad_norm's, for a
+ * clip over all matrices instead of each one alone): g = coef * dW, no norm taken of dW here
+ * (one read of it less).  coef: fp32 [1] on the device.  All else as bitlinear_optimizer_step.
+ * Three launches with gamma, two without. */
+BL_API bl_status bitlinear_optimizer_step_coef(float* W, const float* dW, float* m, float* v,
+                                        int64_t N, int64_t K, float lr, float beta1, float beta2,
+                                        float eps, float weight_decay, const float* coef, int32_t* step,
+                                        int8_t* Wq_i8, uint16_t* Wq_bf16, uint8_t* Wpacked,
+                                        float* gamma, void* ws, size_t ws_bytes, void* stream);
+
+/* ==============================================================================
+ * Global gradient norm over many tensors, and clipping to it (P3 §6, P4 §4.1:
+ * clip_grad_norm_ over the model's parameters, max_norm 1.0):
+ *   norm = sqrt( sum_i sum_j g_ij^2 )            fp64 sums, a fixed order
+ *   coef = min(1, max_norm / (norm + 1e-6)),  1 when max_norm <= 0    (fp64, rounded once)
+ *   out_i = coef * g_i                            fp32 product, rounded to g_i's type
+ * grads, out, numel, dtypes: HOST arrays of `count` device pointers, element counts and types
+ * (read before the call returns).  A gradient has its elements' alignment (not 16 bytes: views
+ * of a flat buffer will do), may be empty, and each may be fp32 or bf16.  out[i] has the type
+ * and size of grads[i] and is grads[i] itself (clipped in place; left unread and unwritten when
+ * coef is 1) or does not overlap any gradient.  norm, coef: fp32 [1] on the device.  Non-finite
+ * gradients are not refused: an infinite norm gives coef = 0, a NaN one NaN, and norm says so.
+ * The same gradients give the same bits on every call and rank, so ranks that hold the same
+ * (all-reduced) gradients take the same step.
+ * ws: at least bitlinear_workspace_bytes(1, 1, 1) bytes, no initialisation needed.
+ * Two launches for up to 64 non-empty gradients, two more for each further 960. */
+BL_API bl_status bitlinear_grad_norm(const void* const* grads, const int64_t* numel, const bl_dtype* dtypes,
+                              int64_t count, float max_norm, float* norm, float* coef,
+                              void* ws, size_t ws_bytes, void* stream);
+BL_API bl_status bitlinear_clip_grads(const void* const* grads, void* const* out, const int64_t* numel,
+                               const bl_dtype* dtypes, int64_t count, float max_norm, float* norm,
+                               float* coef, void* ws, size_t ws_bytes, void* stream);
+
+/* ==============================================================================
+ * The step between two BitLinears of a residual stack: the norm behind a block, its gate and
+ * residual scale, the residual sum, and the norm (and quantiser) in front of the next block
+ * (P3 §3.1's RMSNorm and activation_quant; P5: the residual stream kept in full precision):
+ *   n    = Y * r1_t * g_post,  r1_t = 1 / sqrt(mean_k Y^2 + eps_post)   (n = Y if !post_norm)
+ *   Xout = alpha * X + beta * gate * n                       rounded to x_dt
+ *   h    = Xout * r2_t * g_pre, r2_t = 1 / sqrt(mean_k Xout^2 + eps_pre)
+ * and, of h, either H (rounded to y_dt), or Xq / sx / Xdq as bitlinear_act_quant gives them for
+ * Xout (the int8 operand of bitlinear_linear*), or nothing (H and Xq both NULL).
+ * X, Xout: [T x K] of x_dt; Y, H, Xdq: [T x K] of y_dt; (x_dt, y_dt) is (fp32, fp32),
+ * (bf16, bf16) or (fp32, bf16).  Xout may be X.  gate: per gate_kind, fp32, but [T x K] of y_dt
+ * for BL_GATE_ELEMENT; NULL for BL_GATE_NONE.  g_post, g_pre: fp32 [K] or NULL (gain 1).
+ * r_post fp32 [T] (required with post_norm), r_pre fp32 [T] (required with H or Xq): saved for
+ * the backward.  Xq int8 [T x K], sx fp32 [T] (required with Xq), Xdq optional.
+ * Any 1 <= K <= 16384 (rows that are whole 16-byte vectors, K % 8 == 0, are faster); Xq needs
+ * K % 32 == 0.  Sums of squares in fp64, elements in fp32, one rounding an operation.  One
+ * launch; every input is read once. */
+BL_API bl_status bitlinear_residual_norm(const void* X, bl_dtype x_dt, const void* Y, bl_dtype y_dt,
+                                  int64_t T, int64_t K, int post_norm, const float* g_post, float eps_post,
+                                  bl_gate gate_kind, const void* gate, float alpha, float beta,
+                                  const float* g_pre, float eps_pre, void* Xout, float* r_post, float* r_pre,
+                                  void* H, int8_t* Xq, float* sx, void* Xdq, void* stream);
+
+/* Its gradient, the quantiser passed straight through (dH is then bitlinear_grad_input's dX_hat):
+ *   u2 = Xout r2,  e = g_pre dH,  d = dXout + r2 (e - u2 mean_k(e u2)),   dX = alpha d
+ *   u1 = Y r1,  dn = beta gate d,  e1 = g_post dn,  dY = r1 (e1 - u1 mean_k(e1 u1))
+ *        (dY = dn if !post_norm)
+ *   dg_pre = sum_t dH u2,  dg_post = sum_t dn u1,
+ *   dgate = beta d n summed over what the gate was broadcast over
+ * dXout fp32 [T x K], the gradient of Xout that arrives past the next block, or NULL (the top of
+ * the stack); dH fp32 [T x K], or NULL (no norm output was used); not both NULL.  Xout (read
+ * only with dH), Y, gate, the gains and r_post / r_pre as in the forward.  dX fp32 [T x K] (may
+ * be dXout or dH); dY [T x K] of y_dt (the operand of the block's own backward).  Optional: dg_post,
+ * dg_pre fp32 [K]; dgate, shaped and typed as the gate.  ws: at least
+ * bitlinear_workspace_bytes(T, 16, K) bytes when dg_post, dg_pre or the gradient of a scalar or
+ * channel gate is asked for.  Column sums are fp32 in each of at most 148 blocks and joined in
+ * block order: repeatable.  One launch, or two with column sums. */
+BL_API bl_status bitlinear_residual_norm_backward(const float* dXout, const float* dH, const void* Xout,
+                                           bl_dtype x_dt, const void* Y, bl_dtype y_dt, int64_t T, int64_t K,
+                                           int post_norm, const float* g_post, const float* r_post,
+                                           bl_gate gate_kind, const void* gate, float alpha, float beta,
+                                           const float* g_pre, const float* r_pre, float* dX, void* dY,
+                                           float* dg_post, float* dg_pre, void* dgate,
+                                           void* ws, size_t ws_bytes, void* stream);
+
+/* ==============================================================================
+ * 8-bit linear: scales for each token and each channel, for the layers that stay in 8 bits
+ * beside ternary ones (P4, P5: mixed 8-bit layers).
+ * Weight quantiser (activation_quant's rule, P3 §2.2, over the rows of W):
+ *   m_n = max(max_k |W[n,k]|, 1e-5);  gamma_rows[n] = fl32(m_n / 127)
+ *   W_q[n,k] = round( fl32(W[n,k] * fl32(127 / m_n)) )          in [-127, 127]
+ * Outputs: Wq_i8 int8 [N x K] and Wq_bf16 = W_q * bf16(gamma_rows[n]) (bf16 bits, the operand of
+ * bitlinear_grad_input with a gamma of 1.0), both optional; gamma_rows fp32 [N].  One launch. */
+BL_API bl_status bitlinear_quant_weight_int8(const float* W, int64_t N, int64_t K, int8_t* Wq_i8,
+                                      uint16_t* Wq_bf16, float* gamma_rows, void* stream);
+
+/* The product, from one token to a whole prompt:
+ *   acc[t,n] = sum_k Xq[t,k] * W_q[n,k]                          exact int32 (codes -128..127)
+ *   Y[t,n]   = fl32( (float)acc[t,n] * fl32(gamma_rows[n] / sx[t]) )    rounded to y_dt
+ * Xq int8 [T x K], sx fp32 [T] (bitlinear_act_quant's or bitlinear_residual_norm's), Wq_i8 int8
+ * [N x K], gamma_rows fp32 [N], Y [T x N] of y_dt, acc int32 [T x N] optional.  K < 2^17 (the
+ * int32 sums cannot wrap).  One launch. */
+BL_API bl_status bitlinear_linear_int8(const int8_t* Xq, const float* sx, int64_t T, int64_t K,
+                                const int8_t* Wq_i8, const float* gamma_rows, int64_t N,
+                                void* Y, bl_dtype y_dt, int32_t* acc, void* stream);
 
 /* ------------------------------------------------------------------------------
  * Tensor-pipe peak probe (a measurement kernel with no counterpart on the pages): one
