@@ -102,7 +102,7 @@ def lib():
 
 def call(name: str, *args) -> None:
     """Call an entry point that returns bl_status; raise BitLinearError unless BL_OK."""
-    L = lib()
+    L = _lib if _lib is not None else lib()
     st = getattr(L, name)(*args)
     if st != BL_OK:
         raise BitLinearError(name, st, L.bl_last_error().decode(errors="replace"))

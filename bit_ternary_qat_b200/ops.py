@@ -42,19 +42,23 @@ def _stream(device) -> int:
 
 def _same(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
     """Address of a contiguous tensor of this type, shape and device; raises if it is another."""
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream().cuda_stream without the Stream object
 
 
 def _call(dev, name: str, *args) -> None:
     """Call an entry point on the current stream of the tensors' device, that device current."""
-    if torch.cuda.current_device() == dev.index:
-        _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+    i = dev.index
+    if torch.cuda.current_device() == i:
+        _lib.call(name, *args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            _lib.call(name, *args, torch.cuda.current_stream(dev).cuda_stream)
+            _lib.call(name, *args, _raw_stream(i))
 
 
 def workspace_bytes(T: int, N: int, K: int) -> int:
@@ -478,31 +482,45 @@ def _grad_lists(grads, out):
     if n == 0:
         raise ValueError("grads must not be empty")
     dev = grads[0].device
-    if out is not None and len(out) != n:
-        raise ValueError(f"out must have {n} tensors, got {len(out)}")
-    for i, g in enumerate(grads):
-        if g.device != dev or not g.is_cuda:
-            raise ValueError(f"grads[{i}] must be a CUDA tensor on {dev}, got {g.device}")
-        if g.dtype not in _DT:
-            raise ValueError(f"grads[{i}]: unsupported dtype {g.dtype}")
-        if not g.is_contiguous():
-            raise ValueError(f"grads[{i}] must be contiguous")
-        if out is not None:
-            _same(out[i], f"out[{i}]", g.dtype, g.shape, dev)
-    ptrs = (_lib.P * n)(*[g.data_ptr() for g in grads])
-    outs = (_lib.P * n)(*[t.data_ptr() for t in out]) if out is not None else ptrs
-    return dev, ptrs, outs, (_lib.I64 * n)(*[g.numel() for g in grads]), (_lib.INT * n)(*[_DT[g.dtype] for g in grads])
+    numel, types = [g.numel() for g in grads], [g.dtype for g in grads]
+    every = grads
+    if out is not None:
+        if [t.numel() for t in out] != numel or [t.dtype for t in out] != types:
+            raise ValueError("out must have the sizes and types of grads")
+        every = [*grads, *out]
+    where = dev.index
+    for t in every:
+        if t.get_device() != where or not t.is_contiguous():
+            raise ValueError(f"gradients and outputs must be contiguous CUDA tensors on one device, got {t.device}, "
+                             f"strides {t.stride()}")
+    try:
+        codes = [_DT[t] for t in types]
+    except KeyError as e:
+        raise ValueError(f"unsupported dtype {e.args[0]}") from None
+    if where is None or where < 0:
+        raise ValueError("grads must be CUDA tensors")
+    return (dev, [g.data_ptr() for g in grads], None if out is None else [t.data_ptr() for t in out],
+            (_lib.I64 * n)(*numel), (_lib.INT * n)(*codes))
+
+
+# the clip's workspace is the same for every list
+_CLIP_WS = None
 
 
 def _norm_outputs(dev, norm, coef, ws):
+    global _CLIP_WS
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
+    else:
+        _same(norm, "norm", torch.float32, (1,), dev)
     if coef is None:
-        coef = torch.empty(1, dtype=torch.float32, device=dev)
+        coef = torch.empty_like(norm)
+    else:
+        _same(coef, "coef", torch.float32, (1,), dev)
     if ws is None:
-        ws = workspace(1, 1, 1, dev)
-    _same(norm, "norm", torch.float32, (1,), dev)
-    _same(coef, "coef", torch.float32, (1,), dev)
+        if _CLIP_WS is None:
+            _CLIP_WS = workspace_bytes(1, 1, 1)
+        ws = torch.empty(_CLIP_WS, dtype=torch.uint8, device=dev)
     return norm, coef, ws
 
 
@@ -512,7 +530,8 @@ def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tenso
     Returns dict(norm [1] f32, coef [1] f32); coef goes into bitlinear_optimizer_step."""
     dev, ptrs, _, numel, types = _grad_lists(grads, None)
     norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    _call(dev, "bitlinear_grad_norm", ptrs, numel, types, len(grads), max_norm, norm.data_ptr(), coef.data_ptr(),
+    n = len(ptrs)
+    _call(dev, "bitlinear_grad_norm", (_lib.P * n)(*ptrs), numel, types, n, max_norm, norm.data_ptr(), coef.data_ptr(),
           ws.data_ptr(), ws.numel() * ws.element_size())
     return {"norm": norm, "coef": coef}
 
@@ -522,10 +541,14 @@ def bitlinear_clip_grads(grads, max_norm: float = 1.0, out=None, norm: Optional[
     """Scales a list of gradients by the clip coefficient of their global norm, in place or into
     ``out``.  Returns dict(norm [1] f32, coef [1] f32, grads: the scaled list)."""
     dev, ptrs, outs, numel, types = _grad_lists(grads, out)
-    if len({p for p, n in zip(outs, numel) if n}) != sum(1 for n in numel if n):
+    if outs is None:
+        outs = ptrs
+    n = len(ptrs)
+    if len(set(outs)) != n and len({p for p, k in zip(outs, numel) if k}) != sum(1 for k in numel if k):
         raise ValueError("a gradient is written twice")
     norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    _call(dev, "bitlinear_clip_grads", ptrs, outs, numel, types, len(grads), max_norm, norm.data_ptr(),
+    arr = _lib.P * n
+    _call(dev, "bitlinear_clip_grads", arr(*ptrs), arr(*outs), numel, types, n, max_norm, norm.data_ptr(),
           coef.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return {"norm": norm, "coef": coef, "grads": grads if out is None else out}
 
@@ -572,33 +595,48 @@ def bitlinear_residual_norm(x: torch.Tensor, y: torch.Tensor, post_norm: bool = 
     out["x"] may be x itself."""
     shape, dev = _residual_types(x, y)
     T, K = shape
-    o = {} if out is None else dict(out)
-    row, f32 = (T,), torch.float32
-
-    def buf(name, sh, dtype):
-        t = o.get(name)
-        if t is None:
-            t = o[name] = torch.empty(sh, dtype=dtype, device=dev)
-            return t.data_ptr()
-        return _same(t, name, dtype, sh, dev)
-
-    px, py = _same(x, "x", x.dtype, shape, dev), _same(y, "y", y.dtype, shape, dev)
-    kind, pgate = _gate(gate, T, K, y.dtype, dev)
-    r_post = r_pre = h = xq = sx = xdq = None
-    if post_norm:
-        r_post = buf("r_post", row, f32)
-    if mode == "quant":
-        r_pre, xq, sx = buf("r_pre", row, f32), buf("xq", shape, torch.int8), buf("sx", row, f32)
-        if want_xdq:
-            xdq = buf("xdq", shape, y.dtype)
-    elif mode == "norm":
-        r_pre, h = buf("r_pre", row, f32), buf("h", shape, y.dtype)
-    elif mode != "none":
+    xt, yt, f32, row = x.dtype, y.dtype, torch.float32, (T,)
+    px, py = _same(x, "x", xt, shape, dev), _same(y, "y", yt, shape, dev)
+    kind, pgate = (GATE_NONE, None) if gate is None else _gate(gate, T, K, yt, dev)
+    p_post = None if g_post is None else _same(g_post, "g_post", f32, (K,), dev)
+    p_pre = None if g_pre is None else _same(g_pre, "g_pre", f32, (K,), dev)
+    if mode not in ("quant", "norm", "none"):
         raise ValueError(f"mode must be 'quant', 'norm' or 'none', got {mode!r}")
-    _call(dev, "bitlinear_residual_norm", px, _DT[x.dtype], py, _DT[y.dtype], T, K, 1 if post_norm else 0,
-          None if g_post is None else _same(g_post, "g_post", f32, (K,), dev), eps_post, kind, pgate, alpha, beta,
-          None if g_pre is None else _same(g_pre, "g_pre", f32, (K,), dev), eps_pre, buf("x", shape, x.dtype), r_post,
-          r_pre, h, xq, sx, xdq)
+    o = {} if out is None else dict(out)
+    if out is not None:
+        for name, dtype in (("x", xt), ("h", yt), ("xq", torch.int8), ("xdq", yt)):
+            if name in o:
+                _same(o[name], name, dtype, shape, dev)
+        for name in ("r_post", "r_pre", "sx"):
+            if name in o:
+                _same(o[name], name, f32, row, dev)
+    r_post = r_pre = h = xq = sx = xdq = None
+    if "x" not in o:
+        o["x"] = torch.empty_like(x)
+    if post_norm:
+        if "r_post" not in o:
+            o["r_post"] = x.new_empty(row, dtype=f32)
+        r_post = o["r_post"].data_ptr()
+    if mode != "none":
+        if "r_pre" not in o:
+            o["r_pre"] = torch.empty_like(o["r_post"]) if post_norm else x.new_empty(row, dtype=f32)
+        r_pre = o["r_pre"].data_ptr()
+    if mode == "norm":
+        if "h" not in o:
+            o["h"] = torch.empty_like(y)
+        h = o["h"].data_ptr()
+    elif mode == "quant":
+        if "xq" not in o:
+            o["xq"] = x.new_empty(shape, dtype=torch.int8)
+        if "sx" not in o:
+            o["sx"] = torch.empty_like(o["r_pre"])
+        xq, sx = o["xq"].data_ptr(), o["sx"].data_ptr()
+        if want_xdq:
+            if "xdq" not in o:
+                o["xdq"] = torch.empty_like(y)
+            xdq = o["xdq"].data_ptr()
+    _call(dev, "bitlinear_residual_norm", px, _DT[xt], py, _DT[yt], T, K, 1 if post_norm else 0, p_post, eps_post, kind,
+          pgate, alpha, beta, p_pre, eps_pre, o["x"].data_ptr(), r_post, r_pre, h, xq, sx, xdq)
     return o
 
 
@@ -616,33 +654,47 @@ def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[to
     dgate as the gate).  out["dx"] may be dx or dh."""
     shape, dev = _residual_types(x, y)
     T, K = shape
-    o = {} if out is None else dict(out)
-    f32 = torch.float32
-
-    def buf(name, sh, dtype):
-        t = o.get(name)
-        if t is None:
-            t = o[name] = torch.empty(sh, dtype=dtype, device=dev)
-            return t.data_ptr()
-        return _same(t, name, dtype, sh, dev)
+    xt, yt, f32, col = x.dtype, y.dtype, torch.float32, (K,)
 
     def opt(t, name, sh):
         return None if t is None else _same(t, name, f32, sh, dev)
 
+    px, py = _same(x, "x", xt, shape, dev), _same(y, "y", yt, shape, dev)
+    p_dx, p_dh = opt(dx, "dx", shape), opt(dh, "dh", shape)
+    p_post, p_pre = opt(r_post, "r_post", (T,)), opt(r_pre, "r_pre", (T,))
     if dh is not None and r_pre is None:
         raise ValueError("dh needs r_pre")
-    kind, pgate = _gate(gate, T, K, y.dtype, dev)
-    dg_post = buf("dpost_gain", (K,), f32) if want_dgains and r_post is not None else None
-    dg_pre = buf("dpre_gain", (K,), f32) if want_dgains and dh is not None else None
-    dgate = buf("dgate", gate.shape, gate.dtype) if want_dgate and gate is not None else None
-    if ws is None and (dg_post is not None or dg_pre is not None or
-                       (dgate is not None and kind in (GATE_SCALAR, GATE_CHANNEL))):
-        ws = workspace(T, 16, K, dev)
-    _call(dev, "bitlinear_residual_norm_backward", opt(dx, "dx", shape), opt(dh, "dh", shape),
-          _same(x, "x", x.dtype, shape, dev), _DT[x.dtype], _same(y, "y", y.dtype, shape, dev), _DT[y.dtype], T, K,
-          0 if r_post is None else 1, opt(g_post, "g_post", (K,)), opt(r_post, "r_post", (T,)), kind, pgate, alpha,
-          beta, opt(g_pre, "g_pre", (K,)), opt(r_pre, "r_pre", (T,)), buf("dx", shape, f32), buf("dy", shape, y.dtype),
-          dg_post, dg_pre, dgate, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    kind, pgate = (GATE_NONE, None) if gate is None else _gate(gate, T, K, yt, dev)
+    want_post, want_pre = want_dgains and r_post is not None, want_dgains and dh is not None
+    want_dgate = want_dgate and gate is not None
+    o = {} if out is None else dict(out)
+    if out is not None:
+        for name, sh, dtype in (("dx", shape, f32), ("dy", shape, yt), ("dpost_gain", col, f32),
+                                ("dpre_gain", col, f32)) + ((("dgate", gate.shape, gate.dtype),) if want_dgate else ()):
+            if name in o:
+                _same(o[name], name, dtype, sh, dev)
+    if "dx" not in o:
+        o["dx"] = torch.empty_like(dh if dx is None else dx) if dx is not None or dh is not None else x.new_empty(
+            shape, dtype=f32)
+    if "dy" not in o:
+        o["dy"] = torch.empty_like(y)
+    if want_post and "dpost_gain" not in o:
+        o["dpost_gain"] = x.new_empty(col, dtype=f32)
+    if want_pre and "dpre_gain" not in o:
+        o["dpre_gain"] = x.new_empty(col, dtype=f32)
+    if want_dgate and "dgate" not in o:
+        o["dgate"] = torch.empty_like(gate)
+    ws_bytes = 0
+    if ws is None:
+        if want_post or want_pre or (want_dgate and kind in (GATE_SCALAR, GATE_CHANNEL)):
+            ws = workspace(T, 16, K, dev)
+    if ws is not None:
+        ws_bytes = ws.numel() * ws.element_size()
+    _call(dev, "bitlinear_residual_norm_backward", p_dx, p_dh, px, _DT[xt], py, _DT[yt], T, K,
+          0 if r_post is None else 1, opt(g_post, "g_post", col), p_post, kind, pgate, alpha, beta,
+          opt(g_pre, "g_pre", col), p_pre, o["dx"].data_ptr(), o["dy"].data_ptr(),
+          o["dpost_gain"].data_ptr() if want_post else None, o["dpre_gain"].data_ptr() if want_pre else None,
+          o["dgate"].data_ptr() if want_dgate else None, _ptr(ws), ws_bytes)
     return o
 
 
@@ -662,7 +714,7 @@ def bitlinear_quant_weight_int8(W: torch.Tensor, want_i8: bool = True, want_bf16
         if name in o:
             _same(o[name], name, dtype, shape, dev)
         elif want:
-            o[name] = torch.empty(shape, dtype=dtype, device=dev)
+            o[name] = W.new_empty(shape, dtype=dtype)
     _call(dev, "bitlinear_quant_weight_int8", W.data_ptr(), N, K, _ptr(o.get("wq_i8")), _ptr(o.get("wq_bf16")),
           o["gamma_rows"].data_ptr())
     return o
@@ -678,14 +730,20 @@ def bitlinear_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tenso
     dev = xq.device
     T, K = xq.shape
     N = wq_i8.shape[0]
+    px, pw = _same(xq, "xq", torch.int8, (T, K), dev), _same(wq_i8, "wq_i8", torch.int8, (N, K), dev)
+    ps, pg = _same(sx, "sx", torch.float32, (T,), dev), _same(gamma_rows, "gamma_rows", torch.float32, (N,), dev)
     if y is None:
-        y = torch.empty(T, N, dtype=out_dtype, device=dev)
-    if want_acc and acc is None:
-        acc = torch.empty(T, N, dtype=torch.int32, device=dev)
-    _call(dev, "bitlinear_linear_int8", _same(xq, "xq", torch.int8, (T, K), dev),
-          _same(sx, "sx", torch.float32, (T,), dev), T, K, _same(wq_i8, "wq_i8", torch.int8, (N, K), dev),
-          _same(gamma_rows, "gamma_rows", torch.float32, (N,), dev), N, _same(y, "y", y.dtype, (T, N), dev), _dt(y),
-          None if acc is None else _same(acc, "acc", torch.int32, (T, N), dev))
+        y = xq.new_empty((T, N), dtype=out_dtype)
+        py = y.data_ptr()
+    else:
+        py = _same(y, "y", y.dtype, (T, N), dev)
+    pa = None
+    if acc is not None:
+        pa = _same(acc, "acc", torch.int32, (T, N), dev)
+    elif want_acc:
+        acc = xq.new_empty((T, N), dtype=torch.int32)
+        pa = acc.data_ptr()
+    _call(dev, "bitlinear_linear_int8", px, ps, T, K, pw, pg, N, py, _dt(y), pa)
     return y, acc
 
 
