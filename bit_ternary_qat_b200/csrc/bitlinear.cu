@@ -888,24 +888,87 @@ void launch_residual_norm_v(const bl::RnFwdArgs& a, cudaStream_t st) {
         pdl_launch(bl::residual_norm_kernel<kBf16X, kBf16Y, kWarpRow, E, NT, VPT, false>, grid, dim3(NT), 0, st, a);
 }
 
+constexpr size_t kRnSmem = 224 * 1024;   // dynamic shared memory of a ring block (1 KB static beside it)
+
+// The ring kernel: as many row groups, then stages, as shared memory holds beside the gains.
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kGateElem, bool kSm>
+bl_status launch_residual_norm_ring_v(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
+    auto kern = bl::residual_norm_ring_kernel<kBf16X, kBf16Y, TG, kMaxThreads, EPT, kGateElem, kSm>;
+    const size_t row = (size_t)a.K * ((kBf16X ? 2 : 4) + (kBf16Y ? 2 : 4) * (kGateElem ? 2 : 1));
+    const size_t gains = kSm ? (size_t)a.K * 8 : 0;
+    constexpr size_t limit = kRnSmem;
+    const int groups = (int)std::max<size_t>(1, std::min<size_t>(kMaxThreads / TG, (limit - gains) / row));
+    const int stages = (int)std::max<size_t>(1, std::min<size_t>(bl::kRnMaxStages, (limit - gains) / (row * groups)));
+    const size_t smem = gains + row * groups * stages;
+    BL_REQUIRE(smem <= limit, BL_ERR_DEVICE, "residual norm: shared memory too small");
+    static std::atomic<uint64_t> attr_set{0};   // bit d: attribute set on device d
+    int dev_id = 0;
+    cudaGetDevice(&dev_id);
+    if (!(attr_set.load() & (1ull << dev_id))) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
+        if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        attr_set.fetch_or(1ull << dev_id);
+    }
+    const int64_t blocks = std::min<int64_t>((a.T + groups - 1) / groups, dev.sms);
+    pdl_launch(kern, dim3((unsigned)blocks), dim3((unsigned)(TG * groups)), smem, st, a, stages, g_wait_ns.load());
+    return launched("residual_norm_ring");
+}
+
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm = true>
+bl_status launch_residual_norm_ring(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
+    if (a.gate_kind == bl::kGateElement)
+        return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, true, kSm>(a, st, dev);
+    return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, false, kSm>(a, st, dev);
+}
+
 // Rows of whole 16-byte vectors (8 elements) take the vector kernels, others one element at a
 // time; a warp per short row, a block per long one.
 template <bool kBf16X, bool kBf16Y>
-void launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st) {
-    if (a.K % 8 != 0) {
-        if (a.K <= 128) return launch_residual_norm_v<kBf16X, kBf16Y, true, 1, 256, 4>(a, st);
-        if (a.K <= 1024) return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 256, 4>(a, st);
-        if (a.K <= 4096) return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 4>(a, st);
-        return launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 16>(a, st);
-    }
+bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
     const int nvec = a.K / 8;
-    if (nvec <= 32) return launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 1>(a, st);
-    if (nvec <= 64) return launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 2>(a, st);
-    if (nvec <= 128) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 128, 1>(a, st);
-    if (nvec <= 256) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 256, 1>(a, st);
-    if (nvec <= 512) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 1>(a, st);
-    if (nvec <= 1024) return launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 2>(a, st);
-    launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 1024, 2>(a, st);
+    if (a.K % 8 != 0) {
+        if (a.K <= 128) launch_residual_norm_v<kBf16X, kBf16Y, true, 1, 256, 4>(a, st);
+        else if (a.K <= 1024) launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 256, 4>(a, st);
+        else if (a.K <= 4096) launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 4>(a, st);
+        else launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 16>(a, st);
+        return launched("residual_norm");
+    }
+    // The ring pays from about a megabyte and a half of elements on (4096 columns: 300 rows 6.3 us
+    // with it, 7.8 without, fp32 beside bf16; 256 columns: 1200 rows 4.3 us, 3.6 without)
+    if ((int64_t)a.T * a.K >= (3 << 19)) {
+        // Elements per thread: 32 amortise a row's reductions and scalars best (16384 x 4096 bf16:
+        // 108 us against 126 with 16), but an fp32 residual beside a bf16 block wants the
+        // registers for more groups with two stages (137 against 161 us).
+        constexpr bool kMixed = kBf16X != kBf16Y;
+        if (nvec <= 32) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 8>(a, st, dev);
+        if (nvec <= 64) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 16>(a, st, dev);
+        if constexpr (kMixed) {
+            if (nvec <= 128) return launch_residual_norm_ring<kBf16X, kBf16Y, 64, 768, 16>(a, st, dev);
+            if (nvec <= 256) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, 768, 16>(a, st, dev);
+            if (nvec <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 256, 768, 16>(a, st, dev);
+            if (nvec <= 1024) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 16>(a, st, dev);
+        } else {
+            if (nvec <= 128) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 32>(a, st, dev);
+            if (nvec <= 256) return launch_residual_norm_ring<kBf16X, kBf16Y, 64, 768, 32>(a, st, dev);
+            if (nvec <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, 768, 32>(a, st, dev);
+            if (nvec <= 1024) return launch_residual_norm_ring<kBf16X, kBf16Y, 256, 768, 32>(a, st, dev);
+        }
+        // Longer rows: the gains in shared memory if a row fits beside them (4096 x 11008, 100 us
+        // against 139 from global memory), two rows at once if two fit (100 against 113 us)
+        const size_t row = (size_t)a.K * ((kBf16X ? 2 : 4) + (kBf16Y ? 2 : 4) * (a.gate_kind == bl::kGateElement ? 2 : 1));
+        const size_t gains = (size_t)a.K * 8;
+        if (2 * row + gains <= kRnSmem) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 32>(a, st, dev);
+        if (row + gains <= kRnSmem) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 512, 32>(a, st, dev);
+        return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 32, false>(a, st, dev);
+    }
+    if (nvec <= 32) launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 1>(a, st);
+    else if (nvec <= 64) launch_residual_norm_v<kBf16X, kBf16Y, true, 8, 256, 2>(a, st);
+    else if (nvec <= 128) launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 128, 1>(a, st);
+    else if (nvec <= 256) launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 256, 1>(a, st);
+    else if (nvec <= 512) launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 1>(a, st);
+    else if (nvec <= 1024) launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 512, 2>(a, st);
+    else launch_residual_norm_v<kBf16X, kBf16Y, false, 8, 1024, 2>(a, st);
+    return launched("residual_norm");
 }
 
 template <bool kBf16X, bool kBf16Y, int E>
@@ -927,9 +990,48 @@ bl_status launch_residual_norm_bwd_walk(const bl::RnBwdArgs& a, cudaStream_t st,
     return launched("residual_norm_bwd");
 }
 
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm>
+bl_status launch_residual_norm_bwd_ring(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G,
+                                        bool* taken) {
+    auto kern = bl::residual_norm_bwd_ring_kernel<kBf16X, kBf16Y, TG, kMaxThreads, EPT, kSm>;
+    const size_t row = (size_t)a.K * ((a.dx != nullptr ? 4 : 0) + (a.dh != nullptr ? 4 + (kBf16X ? 2 : 4) : 0) +
+                                      (kBf16Y ? 2 : 4) * (a.gate_kind == bl::kGateElement ? 2 : 1));
+    const size_t gains = kSm ? (size_t)a.K * 12 : 0;
+    const size_t sums = (size_t)a.K * 12;     // of one group, over the ring at the end
+    int groups = kMaxThreads / TG;
+    while (groups > 1 && (gains + row * groups > kRnSmem || sums * groups > kRnSmem)) --groups;
+    *taken = gains + row * groups <= kRnSmem && sums * groups <= kRnSmem;
+    if (!*taken) return BL_OK;
+    const int stages = (int)std::min<size_t>(bl::kRnMaxStages, (kRnSmem - gains) / (row * groups));
+    const size_t smem = std::max(gains + row * groups * stages, sums * groups);
+    static std::atomic<uint64_t> attr_set{0};   // bit d: attribute set on device d
+    int dev_id = 0;
+    cudaGetDevice(&dev_id);
+    if (!(attr_set.load() & (1ull << dev_id))) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRnSmem);
+        if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        attr_set.fetch_or(1ull << dev_id);
+    }
+    *G = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(dev.sms, (int)bl::kRnMaxBlocks));
+    pdl_launch(kern, dim3((unsigned)*G), dim3((unsigned)(TG * groups)), smem, st, a, stages, g_wait_ns.load());
+    return launched("residual_norm_bwd_ring");
+}
+
 template <bool kBf16X, bool kBf16Y>
 bl_status launch_residual_norm_bwd(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G) {
     if (a.K % 8 != 0) return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 1>(a, st, dev, G);
+    bool taken = false;
+    int v = getenv("BV") ? atoi(getenv("BV")) : 0;
+#define BL_RN(...) BL_TRY((launch_residual_norm_bwd_ring<kBf16X, kBf16Y, __VA_ARGS__>(a, st, dev, G, &taken)))
+    if (a.K <= 256) { if (v == 0) BL_RN(32, 512, 8, true); else BL_RN(32, 512, 16, true); }
+    else if (a.K <= 512) { if (v == 0) BL_RN(64, 512, 8, true); else BL_RN(32, 512, 16, true); }
+    else if (a.K <= 1024) { if (v == 0) BL_RN(128, 512, 8, true); else BL_RN(64, 512, 16, true); }
+    else if (a.K <= 2048) { if (v == 0) BL_RN(256, 512, 8, true); else BL_RN(128, 512, 16, true); }
+    else if (a.K <= 4096) { if (v == 0) BL_RN(512, 512, 8, true); else if (v == 1) BL_RN(256, 512, 16, true); else if (v == 2) BL_RN(512, 512, 8, false); else if (v == 3) BL_RN(512, 1024, 8, true); }
+    else if (a.K <= 8192) { if (v == 0) BL_RN(512, 512, 16, true); else if (v == 1) BL_RN(512, 512, 16, false); else if (v == 2) BL_RN(1024, 1024, 8, false); }
+    else if (a.K <= 12288) BL_RN(512, 512, 24, false);
+#undef BL_RN
+    if (taken) return BL_OK;
     return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 8>(a, st, dev, G);
 }
 
@@ -1631,10 +1733,9 @@ bl_status bitlinear_residual_norm(const void* X, bl_dtype x_dt, const void* Y, b
     a.post = post_norm != 0; a.gate_kind = (int)gate_kind;
     a.alpha = alpha; a.beta = beta; a.eps_post = eps_post; a.eps_pre = eps_pre;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (x_dt == BL_BF16) launch_residual_norm<true, true>(a, st);
-    else if (y_dt == BL_BF16) launch_residual_norm<false, true>(a, st);
-    else launch_residual_norm<false, false>(a, st);
-    return launched("residual_norm");
+    if (x_dt == BL_BF16) return launch_residual_norm<true, true>(a, st, dev);
+    if (y_dt == BL_BF16) return launch_residual_norm<false, true>(a, st, dev);
+    return launch_residual_norm<false, false>(a, st, dev);
 }
 
 bl_status bitlinear_residual_norm_backward(const float* dXout, const float* dH, const void* Xout, bl_dtype x_dt,
