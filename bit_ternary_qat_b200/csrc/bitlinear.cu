@@ -875,7 +875,7 @@ bl_status check_residual(bl_dtype x_dt, bl_dtype y_dt, int64_t T, int64_t K, int
 }
 
 size_t rn_ws_bytes(int64_t K) {
-    return sizeof(double) * bl::kRnMaxBlocks + 3 * sizeof(float) * (size_t)bl::kRnMaxBlocks * (size_t)K;
+    return sizeof(double) * bl::kRnMaxBlocks + 2 * sizeof(float) * (size_t)bl::kRnMaxBlocks * (size_t)K;
 }
 
 template <bool kBf16X, bool kBf16Y, bool kWarpRow, int E, int NT, int VPT>
@@ -890,12 +890,20 @@ void launch_residual_norm_v(const bl::RnFwdArgs& a, cudaStream_t st) {
 
 constexpr size_t kRnSmem = 224 * 1024;   // dynamic shared memory of a ring block (1 KB static beside it)
 
+// Bytes of a row in the forward's ring, and of the gains beside it.
+template <bool kBf16X, bool kBf16Y>
+size_t rn_fwd_row(const bl::RnFwdArgs& a) {
+    const bool odd = a.K % 8 != 0;
+    return bl::rn_pitch(odd, a.K * (kBf16X ? 2u : 4u)) +
+           (size_t)bl::rn_pitch(odd, a.K * (kBf16Y ? 2u : 4u)) * (a.gate_kind == bl::kGateElement ? 2 : 1);
+}
+size_t rn_gain_bytes(int cols) { return 2 * (((size_t)cols * 4 + 15) & ~size_t(15)); }
+
 // The ring kernel: as many row groups, then stages, as shared memory holds beside the gains.
-template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kGateElem, bool kSm>
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kGateElem, bool kSm, bool kOdd>
 bl_status launch_residual_norm_ring_v(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
-    auto kern = bl::residual_norm_ring_kernel<kBf16X, kBf16Y, TG, kMaxThreads, EPT, kGateElem, kSm>;
-    const size_t row = (size_t)a.K * ((kBf16X ? 2 : 4) + (kBf16Y ? 2 : 4) * (kGateElem ? 2 : 1));
-    const size_t gains = kSm ? (size_t)a.K * 8 : 0;
+    auto kern = bl::residual_norm_ring_kernel<kBf16X, kBf16Y, TG, kMaxThreads, EPT, kGateElem, kSm, kOdd>;
+    const size_t row = rn_fwd_row<kBf16X, kBf16Y>(a), gains = kSm ? rn_gain_bytes(a.K) : 0;
     constexpr size_t limit = kRnSmem;
     const int groups = (int)std::max<size_t>(1, std::min<size_t>(kMaxThreads / TG, (limit - gains) / row));
     const int stages = (int)std::max<size_t>(1, std::min<size_t>(bl::kRnMaxStages, (limit - gains) / (row * groups)));
@@ -914,11 +922,11 @@ bl_status launch_residual_norm_ring_v(const bl::RnFwdArgs& a, cudaStream_t st, c
     return launched("residual_norm_ring");
 }
 
-template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm = true>
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm = true, bool kOdd = false>
 bl_status launch_residual_norm_ring(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
     if (a.gate_kind == bl::kGateElement)
-        return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, true, kSm>(a, st, dev);
-    return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, false, kSm>(a, st, dev);
+        return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, true, kSm, kOdd>(a, st, dev);
+    return launch_residual_norm_ring_v<kBf16X, kBf16Y, TG, kMaxThreads, EPT, false, kSm, kOdd>(a, st, dev);
 }
 
 // Rows of whole 16-byte vectors (8 elements) take the vector kernels, others one element at a
@@ -926,16 +934,26 @@ bl_status launch_residual_norm_ring(const bl::RnFwdArgs& a, cudaStream_t st, con
 template <bool kBf16X, bool kBf16Y>
 bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
     const int nvec = a.K / 8;
+    // The ring pays from about a megabyte and a half of elements on (4096 columns: 300 rows 6.3 us
+    // with it, 7.8 without, fp32 beside bf16; 256 columns: 1200 rows 4.3 us, 3.6 without)
+    const bool ring = (int64_t)a.T * a.K >= (3 << 19);
     if (a.K % 8 != 0) {
+        if (ring) {
+            const size_t row = rn_fwd_row<kBf16X, kBf16Y>(a), gains = rn_gain_bytes(a.K);
+            if (a.K <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 512, 16, true, true>(a, st, dev);
+            if (a.K <= 2048) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, 768, 16, true, true>(a, st, dev);
+            if (a.K <= 8192) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 16, true, true>(a, st, dev);
+            if (row + gains <= kRnSmem)
+                return launch_residual_norm_ring<kBf16X, kBf16Y, 1024, 1024, 16, true, true>(a, st, dev);
+            return launch_residual_norm_ring<kBf16X, kBf16Y, 1024, 1024, 16, false, true>(a, st, dev);
+        }
         if (a.K <= 128) launch_residual_norm_v<kBf16X, kBf16Y, true, 1, 256, 4>(a, st);
         else if (a.K <= 1024) launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 256, 4>(a, st);
         else if (a.K <= 4096) launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 4>(a, st);
         else launch_residual_norm_v<kBf16X, kBf16Y, false, 1, 1024, 16>(a, st);
         return launched("residual_norm");
     }
-    // The ring pays from about a megabyte and a half of elements on (4096 columns: 300 rows 6.3 us
-    // with it, 7.8 without, fp32 beside bf16; 256 columns: 1200 rows 4.3 us, 3.6 without)
-    if ((int64_t)a.T * a.K >= (3 << 19)) {
+    if (ring) {
         // Elements per thread: 32 amortise a row's reductions and scalars best (16384 x 4096 bf16:
         // 108 us against 126 with 16), but an fp32 residual beside a bf16 block wants the
         // registers for more groups with two stages (137 against 161 us).
@@ -955,8 +973,7 @@ bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const De
         }
         // Longer rows: the gains in shared memory if a row fits beside them (4096 x 11008, 100 us
         // against 139 from global memory), two rows at once if two fit (100 against 113 us)
-        const size_t row = (size_t)a.K * ((kBf16X ? 2 : 4) + (kBf16Y ? 2 : 4) * (a.gate_kind == bl::kGateElement ? 2 : 1));
-        const size_t gains = (size_t)a.K * 8;
+        const size_t row = rn_fwd_row<kBf16X, kBf16Y>(a), gains = rn_gain_bytes(a.K);
         if (2 * row + gains <= kRnSmem) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 32>(a, st, dev);
         if (row + gains <= kRnSmem) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 512, 32>(a, st, dev);
         return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 32, false>(a, st, dev);
@@ -971,68 +988,105 @@ bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const De
     return launched("residual_norm");
 }
 
-template <bool kBf16X, bool kBf16Y, int E>
-bl_status launch_residual_norm_bwd_walk(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G) {
-    constexpr int NT = 512;
-    auto kern = bl::residual_norm_bwd_walk_kernel<kBf16X, kBf16Y, E, NT>;
-    const size_t smem = 3 * sizeof(float) * (size_t)a.K;
-    static std::atomic<uint64_t> attr_set{0};   // bit d: attribute set on device d
-    int dev_id = 0;
-    cudaGetDevice(&dev_id);
-    if (!(attr_set.load() & (1ull << dev_id))) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             3 * (int)sizeof(float) * (int)kMaxRowK);
-        if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        attr_set.fetch_or(1ull << dev_id);
-    }
-    *G = (int)std::min<int64_t>(a.T, std::min(dev.sms, (int)bl::kRnMaxBlocks));
-    pdl_launch(kern, dim3((unsigned)*G), dim3(NT), smem, st, a);
-    return launched("residual_norm_bwd");
+// Columns of a row that each of cl blocks takes: whole 16-byte vectors of bf16 where the row is.
+int rn_cols(int K, int cl) { return K % 8 != 0 ? (K + cl - 1) / cl : (K / 8 + cl - 1) / cl * 8; }
+
+// Bytes of one row in the backward's ring.
+template <bool kBf16X, bool kBf16Y>
+size_t rn_bwd_row(const bl::RnBwdArgs& a, int cols) {
+    const bool odd = a.K % 8 != 0;
+    const size_t f = bl::rn_pitch(odd, cols * 4u), x = bl::rn_pitch(odd, cols * (kBf16X ? 2u : 4u)),
+                 y = bl::rn_pitch(odd, cols * (kBf16Y ? 2u : 4u));
+    return (a.dx != nullptr ? f : 0) + (a.dh != nullptr ? f + x : 0) + y * (a.gate_kind == bl::kGateElement ? 2 : 1);
 }
 
-template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm>
+// G: partial rows (blocks, or clusters of kCl); Gs: blocks.
+template <bool kBf16X, bool kBf16Y, bool kElem, int TG, int EPT, int kCl, bool kOdd = false>
 bl_status launch_residual_norm_bwd_ring(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G,
-                                        bool* taken) {
-    auto kern = bl::residual_norm_bwd_ring_kernel<kBf16X, kBf16Y, TG, kMaxThreads, EPT, kSm>;
-    const size_t row = (size_t)a.K * ((a.dx != nullptr ? 4 : 0) + (a.dh != nullptr ? 4 + (kBf16X ? 2 : 4) : 0) +
-                                      (kBf16Y ? 2 : 4) * (a.gate_kind == bl::kGateElement ? 2 : 1));
-    const size_t gains = kSm ? (size_t)a.K * 12 : 0;
-    const size_t sums = (size_t)a.K * 12;     // of one group, over the ring at the end
-    int groups = kMaxThreads / TG;
-    while (groups > 1 && (gains + row * groups > kRnSmem || sums * groups > kRnSmem)) --groups;
-    *taken = gains + row * groups <= kRnSmem && sums * groups <= kRnSmem;
-    if (!*taken) return BL_OK;
+                                        int* Gs) {
+    auto kern = bl::residual_norm_bwd_ring_kernel<kBf16X, kBf16Y, TG, EPT, kCl, kElem, kOdd>;
+    const int cols = rn_cols(a.K, kCl);
+    const size_t row = rn_bwd_row<kBf16X, kBf16Y>(a, cols), gains = rn_gain_bytes(cols);
+    int groups = 512 / TG;
+    while (groups > 1 && gains + 2 * row * groups > kRnSmem) --groups;
     const int stages = (int)std::min<size_t>(bl::kRnMaxStages, (kRnSmem - gains) / (row * groups));
-    const size_t smem = std::max(gains + row * groups * stages, sums * groups);
-    static std::atomic<uint64_t> attr_set{0};   // bit d: attribute set on device d
+    const size_t smem = std::max(gains + row * groups * stages, gains * groups);   // the groups' sums at the end
+    BL_REQUIRE(stages >= 2 && smem <= kRnSmem && cols <= TG * EPT, BL_ERR_DEVICE,
+               "residual norm backward: shared memory too small");
+    static std::atomic<int> slots[64] = {};
     int dev_id = 0;
     cudaGetDevice(&dev_id);
-    if (!(attr_set.load() & (1ull << dev_id))) {
+    int n = dev_id >= 0 && dev_id < 64 ? slots[dev_id].load() : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3((unsigned)(TG * groups));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCl;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    if (n == 0) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRnSmem);
         if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        attr_set.fetch_or(1ull << dev_id);
+        n = dev.sms;
+        if (kCl > 1) {
+            cfg.gridDim = dim3((unsigned)(dev.sms / kCl * kCl));
+            cfg.dynamicSmemBytes = kRnSmem;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess)
+                return fail(BL_ERR_CUDA, "cudaOccupancyMaxActiveClusters: %s", cudaGetErrorString(e));
+            if (n < 1) return fail(BL_ERR_DEVICE, "no cluster of %d blocks of the residual norm fits on the device", kCl);
+        }
+        if (dev_id >= 0 && dev_id < 64) slots[dev_id].store(n);
     }
-    *G = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(dev.sms, (int)bl::kRnMaxBlocks));
-    pdl_launch(kern, dim3((unsigned)*G), dim3((unsigned)(TG * groups)), smem, st, a, stages, g_wait_ns.load());
+    *G = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(n, (int)bl::kRnMaxBlocks / kCl));
+    *Gs = *G * kCl;
+    cfg.gridDim = dim3((unsigned)*Gs);
+    cfg.dynamicSmemBytes = smem;
+    cfg.numAttrs = 2;
+    cudaLaunchKernelEx(&cfg, kern, a, cols, stages, g_wait_ns.load());
     return launched("residual_norm_bwd_ring");
 }
 
-template <bool kBf16X, bool kBf16Y>
-bl_status launch_residual_norm_bwd(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G) {
-    if (a.K % 8 != 0) return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 1>(a, st, dev, G);
-    bool taken = false;
-    int v = getenv("BV") ? atoi(getenv("BV")) : 0;
-#define BL_RN(...) BL_TRY((launch_residual_norm_bwd_ring<kBf16X, kBf16Y, __VA_ARGS__>(a, st, dev, G, &taken)))
-    if (a.K <= 256) { if (v == 0) BL_RN(32, 512, 8, true); else BL_RN(32, 512, 16, true); }
-    else if (a.K <= 512) { if (v == 0) BL_RN(64, 512, 8, true); else BL_RN(32, 512, 16, true); }
-    else if (a.K <= 1024) { if (v == 0) BL_RN(128, 512, 8, true); else BL_RN(64, 512, 16, true); }
-    else if (a.K <= 2048) { if (v == 0) BL_RN(256, 512, 8, true); else BL_RN(128, 512, 16, true); }
-    else if (a.K <= 4096) { if (v == 0) BL_RN(512, 512, 8, true); else if (v == 1) BL_RN(256, 512, 16, true); else if (v == 2) BL_RN(512, 512, 8, false); else if (v == 3) BL_RN(512, 1024, 8, true); }
-    else if (a.K <= 8192) { if (v == 0) BL_RN(512, 512, 16, true); else if (v == 1) BL_RN(512, 512, 16, false); else if (v == 2) BL_RN(1024, 1024, 8, false); }
-    else if (a.K <= 12288) BL_RN(512, 512, 24, false);
+template <bool kBf16X, bool kBf16Y, bool kElem>
+bl_status launch_residual_norm_bwd_v(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G, int* Gs) {
+    // the gains and two stages (a row's first pass runs before the last row's stage is given back)
+    auto fits = [&](int cl, int groups) {
+        const int cols = rn_cols(a.K, cl);
+        return rn_gain_bytes(cols) + 2 * rn_bwd_row<kBf16X, kBf16Y>(a, cols) * groups <= kRnSmem;
+    };
+#define BL_RN(...) return launch_residual_norm_bwd_ring<kBf16X, kBf16Y, kElem, __VA_ARGS__>(a, st, dev, G, Gs)
+    if (a.K % 8 != 0) {
+        if (a.K <= 512) BL_RN(32, 16, 1, true);
+        if (a.K <= 2048) BL_RN(128, 16, 1, true);
+        if (a.K <= 8192 && fits(1, 1)) BL_RN(512, 16, 1, true);
+        if (fits(2, 1)) BL_RN(512, 16, 2, true);
+        BL_RN(512, 8, 4, true);
+    }
+    // 16 columns a thread amortise a row's reduction best (16384 x 4096 bf16: 186 us against 200
+    // with 8), as long as two stages of all the groups fit (fp32, 16384 x 2048: 131 against 124)
+    if (a.K <= 256) BL_RN(32, 8, 1);
+    if (a.K <= 512) BL_RN(32, 16, 1);
+    if (a.K <= 1024 && fits(1, 8)) BL_RN(64, 16, 1);
+    if (a.K <= 1024) BL_RN(128, 8, 1);
+    if (a.K <= 2048 && fits(1, 4)) BL_RN(128, 16, 1);
+    if (a.K <= 2048) BL_RN(256, 8, 1);
+    if (a.K <= 4096 && fits(1, 2)) BL_RN(256, 16, 1);
+    if (a.K <= 4096) BL_RN(512, 8, 1);
+    if (a.K <= 8192 && fits(1, 1)) BL_RN(512, 16, 1);
+    if (a.K <= 8192) BL_RN(512, 8, 2);
+    if (fits(2, 1)) BL_RN(512, 16, 2);
+    BL_RN(512, 8, 4);
 #undef BL_RN
-    if (taken) return BL_OK;
-    return launch_residual_norm_bwd_walk<kBf16X, kBf16Y, 8>(a, st, dev, G);
+}
+
+template <bool kBf16X, bool kBf16Y>
+bl_status launch_residual_norm_bwd(const bl::RnBwdArgs& a, cudaStream_t st, const DeviceInfo& dev, int* G, int* Gs) {
+    if (a.gate_kind == bl::kGateElement) return launch_residual_norm_bwd_v<kBf16X, kBf16Y, true>(a, st, dev, G, Gs);
+    return launch_residual_norm_bwd_v<kBf16X, kBf16Y, false>(a, st, dev, G, Gs);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1778,26 +1832,26 @@ bl_status bitlinear_residual_norm_backward(const float* dXout, const float* dH, 
     // the scalar's partials first (fp64), then one [blocks x K] array for each column sum
     uint8_t* w = static_cast<uint8_t*>(ws);
     float* part = reinterpret_cast<float*>(w + sizeof(double) * bl::kRnMaxBlocks);
-    const int64_t rows = bl::kRnMaxBlocks * K;
+    const bool scalar = dgate != nullptr && gate_kind == BL_GATE_SCALAR;
+    const bool channel = dgate != nullptr && gate_kind == BL_GATE_CHANNEL;
     if (dg_pre != nullptr) a.part_pre = part;
-    if (dg_post != nullptr) a.part_post = part + rows;
-    if (dgate != nullptr) {
-        if (gate_kind == BL_GATE_CHANNEL) a.part_gate = part + 2 * rows;
-        else if (gate_kind == BL_GATE_SCALAR) a.part_scalar = reinterpret_cast<double*>(w);
-        else a.dgate = dgate;
-    }
+    if (dg_post != nullptr || channel) a.part_s = part + bl::kRnMaxBlocks * K;
+    if (scalar) a.part_scalar = reinterpret_cast<double*>(w);
+    if (!scalar && !channel) a.dgate = dgate;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    int G = 0;
-    if (x_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<true, true>(a, st, dev, &G)));
-    else if (y_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<false, true>(a, st, dev, &G)));
-    else BL_TRY((launch_residual_norm_bwd<false, false>(a, st, dev, &G)));
+    int G = 0, Gs = 0;
+    if (x_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<true, true>(a, st, dev, &G, &Gs)));
+    else if (y_dt == BL_BF16) BL_TRY((launch_residual_norm_bwd<false, true>(a, st, dev, &G, &Gs)));
+    else BL_TRY((launch_residual_norm_bwd<false, false>(a, st, dev, &G, &Gs)));
     if (!sums) return BL_OK;
     bl::RnReduceArgs r{};
-    r.part[0] = a.part_pre; r.part[1] = a.part_post; r.part[2] = a.part_gate;
-    r.out[0] = dg_pre; r.out[1] = dg_post; r.out[2] = static_cast<float*>(dgate);
-    r.part_scalar = a.part_scalar; r.dscalar = static_cast<float*>(dgate);
-    r.G = G; r.K = (int)K;
-    pdl_launch(bl::rn_reduce_kernel, dim3((unsigned)((K + 31) / 32), 3), dim3(1024), 0, st, r);
+    r.part_pre = a.part_pre; r.part_s = a.part_s; r.part_scalar = a.part_scalar;
+    r.gate = gate_kind == BL_GATE_SCALAR || gate_kind == BL_GATE_CHANNEL ? static_cast<const float*>(gate) : nullptr;
+    r.g_post = g_post;
+    r.dg_pre = dg_pre; r.dg_post = dg_post; r.dgate = scalar || channel ? static_cast<float*>(dgate) : nullptr;
+    r.beta = beta; r.gate_kind = (int)gate_kind;
+    r.G = G; r.Gs = Gs; r.K = (int)K;
+    pdl_launch(bl::rn_reduce_kernel, dim3((unsigned)((K + 31) / 32), 2), dim3(1024), 0, st, r);
     return launched("residual_norm_reduce");
 }
 

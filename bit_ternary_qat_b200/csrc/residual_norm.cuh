@@ -309,10 +309,44 @@ __device__ __forceinline__ V rn_group_reduce(V v, V* red, int g, Op&& op) {
     return v;
 }
 
+// Rows that are no whole 16-byte vectors (kOdd): bulk copies move the aligned bytes around the row,
+// and its elements start `rn_shift` bytes into them.  Room for a row of n bytes in a stage:
+__host__ __device__ constexpr uint32_t rn_pitch(bool odd, uint32_t n) { return odd ? (n + 30u) & ~15u : n; }
+__device__ __forceinline__ uint32_t rn_shift(int64_t first_byte) { return static_cast<uint32_t>(first_byte) & 15u; }
+
+// Where a row's bulk copy reads from: bytes [lo, lo + n) of its array (of `total` bytes, 16-byte
+// aligned base), the aligned bytes around [b0, b1).  The last rows of the array stop at the last
+// whole 16 bytes inside it; what is behind them is copied by the calling thread (at most 15 bytes).
+struct RnSpan {
+    int64_t lo;
+    uint32_t n;
+};
+template <int kSize>
+__device__ __forceinline__ RnSpan rn_span(uint8_t* dst, const uint8_t* src, int64_t b0, int64_t b1, int64_t total) {
+    RnSpan s;
+    s.lo = b0 & ~int64_t(15);
+    int64_t hi = (b1 + 15) & ~int64_t(15);
+    if (hi > total) {
+        hi = total & ~int64_t(15);
+        if (hi < s.lo) hi = s.lo;
+        for (int64_t b = hi > b0 ? hi : b0; b < b1; b += kSize) {
+            if constexpr (kSize == 2)
+                *reinterpret_cast<uint16_t*>(dst + (b - s.lo)) = *reinterpret_cast<const uint16_t*>(src + b);
+            else
+                *reinterpret_cast<uint32_t*>(dst + (b - s.lo)) = *reinterpret_cast<const uint32_t*>(src + b);
+        }
+    }
+    s.n = static_cast<uint32_t>(hi - s.lo);
+    return s;
+}
+
 // E adjacent elements out of shared memory, widened exactly.
 template <bool kBf16, int E>
 __device__ __forceinline__ void rn_lds(const uint8_t* row, int v, float (&f)[E]) {
-    if constexpr (kBf16) {
+    if constexpr (E == 1) {
+        if constexpr (kBf16) f[0] = bf16_bits_to_float(reinterpret_cast<const uint16_t*>(row)[v]);
+        else f[0] = reinterpret_cast<const float*>(row)[v];
+    } else if constexpr (kBf16) {
         uint32_t w[E / 2];
         if constexpr (E == 8) {
             const uint4 a = reinterpret_cast<const uint4*>(row)[v];
@@ -359,7 +393,9 @@ __device__ __forceinline__ void rn_quant_store(const float (&h)[E], float s, flo
 // warp's 16-byte reads are adjacent) or read from global memory.
 template <bool kSm, int E>
 __device__ __forceinline__ void rn_gain(const float* g, int v, int nvec, float (&f)[E]) {
-    if constexpr (kSm) {
+    if constexpr (kSm && E == 1) {
+        f[0] = g[v];
+    } else if constexpr (kSm) {
 #pragma unroll
         for (int i = 0; i < E / 4; ++i) {
             const float4 a = reinterpret_cast<const float4*>(g)[i * nvec + v];
@@ -371,19 +407,20 @@ __device__ __forceinline__ void rn_gain(const float* g, int v, int nvec, float (
 }
 template <int E>
 __device__ __forceinline__ void rn_gain_put(float* g, int v, int nvec, const float (&f)[E]) {
+    if constexpr (E == 1) g[v] = f[0];
 #pragma unroll
     for (int i = 0; i < E / 4; ++i)
         reinterpret_cast<float4*>(g)[i * nvec + v] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
-// Forward for rows of whole vectors: thread i of a group owns vectors i + j * TG of E elements,
-// EPT elements in all.  kSm:
+// Forward: thread i of a group owns vectors i + j * TG of E elements, EPT elements in all (kOdd: the
+// rows are no whole 16-byte vectors, E = 1).  kSm:
 // the weights w (for a gate that is the same in every row) and g2 are formed once per block in
 // shared memory; the rows read them from there.
-template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kGateElem, bool kSm>
+template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kGateElem, bool kSm, bool kOdd>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     residual_norm_ring_kernel(const RnFwdArgs a, int stages, uint64_t wait_ns) {
-    constexpr int E = kBf16X ? 8 : 4;
+    constexpr int E = kOdd ? 1 : kBf16X ? 8 : 4;
     constexpr int VPT = EPT / E;
     constexpr int kRG = kMaxThreads / TG;
     extern __shared__ __align__(128) uint8_t rn_smem[];
@@ -402,20 +439,37 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     pdl_trigger_and_wait();
 
     const int nvec = a.K / E;
-    const uint32_t xb = a.K * (kBf16X ? 2u : 4u), yb = a.K * (kBf16Y ? 2u : 4u);
-    const uint32_t row_bytes = xb + (kGateElem ? 2 * yb : yb);
+    constexpr int xs = kBf16X ? 2 : 4, ys = kBf16Y ? 2 : 4;
+    const uint32_t xb = a.K * xs, yb = a.K * ys;
+    const uint32_t o_y = rn_pitch(kOdd, xb), o_g = o_y + rn_pitch(kOdd, yb);
+    const uint32_t row_bytes = o_g + (kGateElem ? rn_pitch(kOdd, yb) : 0u);
+    const uint32_t gain_bytes = (static_cast<uint32_t>(a.K) * 4u + 15u) & ~15u;
     float* w_sm = reinterpret_cast<float*>(rn_smem);
-    float* g_sm = w_sm + a.K;
-    uint8_t* ring = rn_smem + (kSm ? static_cast<size_t>(a.K) * 8 : 0) + static_cast<size_t>(g) * stages * row_bytes;
+    float* g_sm = reinterpret_cast<float*>(rn_smem + gain_bytes);
+    uint8_t* ring = rn_smem + (kSm ? 2 * gain_bytes : 0) + static_cast<size_t>(g) * stages * row_bytes;
     const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
     const double invK = 1.0 / static_cast<double>(a.K);
     auto issue = [&](int64_t t, int s) {
         uint8_t* dst = ring + static_cast<size_t>(s) * row_bytes;
-        mbar_arrive_expect_tx(&full[g][s], row_bytes);
-        bulk_load(dst, static_cast<const uint8_t*>(a.x) + t * xb, xb, &full[g][s]);
-        bulk_load(dst + xb, static_cast<const uint8_t*>(a.y) + t * yb, yb, &full[g][s]);
-        if constexpr (kGateElem)
-            bulk_load(dst + xb + yb, static_cast<const uint8_t*>(a.gate) + t * yb, yb, &full[g][s]);
+        uint64_t* bar = &full[g][s];
+        const uint8_t *xg = static_cast<const uint8_t*>(a.x), *yg = static_cast<const uint8_t*>(a.y),
+                      *gg = static_cast<const uint8_t*>(a.gate);
+        if constexpr (kOdd) {
+            const int64_t rows = a.T;
+            const RnSpan sx = rn_span<xs>(dst, xg, t * xb, (t + 1) * xb, rows * xb);
+            const RnSpan sy = rn_span<ys>(dst + o_y, yg, t * yb, (t + 1) * yb, rows * yb);
+            RnSpan sg{0, 0};
+            if constexpr (kGateElem) sg = rn_span<ys>(dst + o_g, gg, t * yb, (t + 1) * yb, rows * yb);
+            mbar_arrive_expect_tx(bar, sx.n + sy.n + sg.n);
+            if (sx.n) bulk_load(dst, xg + sx.lo, sx.n, bar);
+            if (sy.n) bulk_load(dst + o_y, yg + sy.lo, sy.n, bar);
+            if (sg.n) bulk_load(dst + o_g, gg + sg.lo, sg.n, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, row_bytes);
+            bulk_load(dst, xg + t * xb, xb, bar);
+            bulk_load(dst + o_y, yg + t * yb, yb, bar);
+            if constexpr (kGateElem) bulk_load(dst + o_g, gg + t * yb, yb, bar);
+        }
     };
     const int64_t t_first = static_cast<int64_t>(blockIdx.x) * RG + g;
     if (tid == 0)
@@ -461,8 +515,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     for (int64_t t = t_first; t < a.T; t += step, par ^= 1u) {
         if (row_gate) gs = __fmul_rn(__ldg(static_cast<const float*>(a.gate) + t), a.beta);
         mbar_wait(&full[g][s], ph, wait_ns, &abort_flag);
-        const uint8_t* xs = ring + static_cast<size_t>(s) * row_bytes;
-        const uint8_t* ys = xs + xb;
+        const uint8_t* stage = ring + static_cast<size_t>(s) * row_bytes;
+        const uint8_t* xr = stage + (kOdd ? rn_shift(t * xb) : 0u);
+        const uint8_t* yr = stage + o_y + (kOdd ? rn_shift(t * yb) : 0u);
         const int64_t row0 = t * nvec;
         float r1 = 1.0f;
         if (a.post) {
@@ -472,7 +527,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 const int v = tid + j * TG;
                 if (v >= nvec) continue;
                 float y[E];
-                rn_lds<kBf16Y, E>(ys, v, y);
+                rn_lds<kBf16Y, E>(yr, v, y);
 #pragma unroll
                 for (int e = 0; e < E; ++e) ss = fma(static_cast<double>(y[e]), static_cast<double>(y[e]), ss);
             }
@@ -488,13 +543,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             const int v = tid + j * TG;
             if (v >= nvec) continue;
             float n[E], w[E];
-            rn_lds<kBf16X, E>(xs, v, x[j]);
-            rn_lds<kBf16Y, E>(ys, v, n);
+            rn_lds<kBf16X, E>(xr, v, x[j]);
+            rn_lds<kBf16Y, E>(yr, v, n);
             if constexpr (kSm) rn_gain<true, E>(w_sm, v, nvec, w);
             else col_weight(v, w);
             if constexpr (kGateElem) {
                 float q[E];
-                rn_lds<kBf16Y, E>(ys + yb, v, q);
+                rn_lds<kBf16Y, E>(yr + (o_g - o_y), v, q);
 #pragma unroll
                 for (int e = 0; e < E; ++e) w[e] = __fmul_rn(__fmul_rn(q[e], a.beta), w[e]);
             } else if (row_gate) {
@@ -542,7 +597,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             }
             if (a.h != nullptr) rn_store<kBf16Y, E>(a.h, row0 + v, x[j]);
         }
-        if (a.xq == nullptr) continue;
+        if (kOdd || a.xq == nullptr) continue;    // codes need K % 32 == 0
         // without a gain rounding is monotone: max |fl(x' r2)| = fl(max |x'| r2)
         if (a.g_pre == nullptr) m = __fmul_rn(mx, r2);
         m = rn_group_reduce<TG>(m, red_m[g][par], g, [](float p, float q) { return fmaxf(p, q); });
@@ -551,7 +606,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * TG;
-            if (v < nvec) rn_quant_store<kBf16Y, E>(x[j], sc, c, a.xq, a.xdq, row0 + v);
+            if constexpr (!kOdd)
+                if (v < nvec) rn_quant_store<kBf16Y, E>(x[j], sc, c, a.xq, a.xdq, row0 + v);
         }
     }
     if (tid == 0 && abort_flag != 0) {
@@ -564,13 +620,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------
-// Backward.  With u1 = y r1, n = u1 g1 (n = y without the post norm), u2 = x' r2:
-//   e  = g2 dh,  c2 = mean_k(e u2)
-//   d  = dx' + r2 (e - u2 c2)          gradient of the new residual (dx' or dh may be absent)
-//   dX = alpha d;   p = beta d
-//   dgate = sum p n over what the gate was broadcast over
-//   dn = p gate;  e1 = g1 dn,  c1 = mean_k(e1 u1);  dY = r1 (e1 - u1 c1)   (dY = dn without)
-//   dg2 = sum_t dh u2,   dg1 = sum_t dn u1
+// Backward.  With u1 = y r1, u2 = x' r2:
+//   c2 = mean_k(g2 dh u2),   d = dx' + r2 (g2 dh - u2 c2)     gradient of the new residual
+//   dX = alpha d
+//   dn = beta gate d,  c1 = mean_k(g1 dn u1),  dY = r1 (g1 dn - u1 c1)    (dY = dn without)
+//   dg2 = sum_t dh u2,   dg1 = sum_t dn u1,   dgate = sum beta d g1 u1 over what it was given for
+// (dx' or dh may be absent).  In the kernels' terms: q = d u1 and
+//   w = beta gate g1 where the gate is the same in every row, else beta g1;  f the token's gate or 1
+//   dY = f r1 (w d - u1 mean_k(w q)),   token gate's gradient = sum_k w q
+// and one column sum S = sum_t f q serves both learned vectors behind the block:
+//   dg1 = beta gate S,   dgate = beta g1 S   (channel; its sum over k for a scalar).
+// An element's gate multiplies w d and the sums' terms, and its gradient is w q.
 // ------------------------------------------------------------------------------------
 struct RnBwdArgs {
     const float* dx;      // [T x K] gradient of x' from the residual stream, or NULL
@@ -584,362 +644,298 @@ struct RnBwdArgs {
     const float* g_pre;
     float* dX;            // [T x K] (may be dx or dh)
     void* dY;             // [T x K] y's type
-    void* dgate;          // token: fp32 [T]; element: [T x K] y's type (channel / scalar: through the partials)
+    void* dgate;          // token: fp32 [T]; element: [T x K] y's type; else NULL
     float* part_pre;      // [G x K] partial sums of dg2, or NULL
-    float* part_post;     // [G x K] of dg1, or NULL
-    float* part_gate;     // [G x K] of the channel gate's gradient, or NULL
-    double* part_scalar;  // [G] of the scalar gate's gradient, or NULL
+    float* part_s;        // [G x K] of S, or NULL
+    double* part_scalar;  // [blocks] of sum_k g1 S, or NULL
     int T, K;
     int post, gate_kind;
     float alpha, beta;
 };
 
-constexpr int kRnMaxBlocks = 148;   // partial rows: three gains' partials fit the RMSNorm backward's workspace
+constexpr int kRnMaxBlocks = 148;   // partial rows
 
-template <int NT>
-__device__ __forceinline__ void rn_block_sum2(float& a, float& b, float (*red)[NT / 32]) {
-    a = warp_sum(a);
-    b = warp_sum(b);
-    if ((threadIdx.x & 31) == 0) {
-        red[0][threadIdx.x >> 5] = a;
-        red[1][threadIdx.x >> 5] = b;
-    }
-    __syncthreads();
-    a = b = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-        a += red[0][w];
-        b += red[1][w];
-    }
+// w of column k as far as it is the same in every row.
+__device__ __forceinline__ float rn_col_w(const RnBwdArgs& a, int k) {
+    float w = a.beta;
+    if (a.gate_kind == kGateScalar) w *= __ldg(static_cast<const float*>(a.gate));
+    if (a.gate_kind == kGateChannel) w *= __ldg(static_cast<const float*>(a.gate) + k);
+    return a.g_post != nullptr ? w * __ldg(a.g_post + k) : w;
 }
 
-// Any row length: the row is walked three times (the second and third time out of L2), and the
-// column sums sit in shared memory, each element owned by one thread.  Block b takes rows b,
-// b + G, ...; the reductions' order is fixed.
-template <bool kBf16X, bool kBf16Y, int E, int NT>
-__global__ void __launch_bounds__(NT) residual_norm_bwd_walk_kernel(const RnBwdArgs a) {
-    extern __shared__ float acc[];               // [3][K]: dg2, dg1, channel gate
-    __shared__ float red[2][2][NT / 32];
-    __shared__ double red_s[NT / 32];
-    pdl_trigger_and_wait();
-    float* acc_pre = acc;
-    float* acc_post = acc + a.K;
-    float* acc_gate = acc + 2 * static_cast<int64_t>(a.K);
-    const int nvec = a.K / E;
-    const float K = static_cast<float>(a.K);
-    for (int i = threadIdx.x; i < 3 * nvec; i += NT)
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[i * E + e] = 0.0f;
-    __syncthreads();
-    double scalar = 0.0;
-
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const int64_t row0 = static_cast<int64_t>(t) * nvec;
-        const float r2 = a.dh != nullptr ? __ldg(a.r_pre + t) : 0.0f;
-        const float r1 = a.post ? __ldg(a.r_post + t) : 1.0f;
-        float gs = 1.0f;
-        if (a.gate_kind == kGateScalar) gs = __ldg(static_cast<const float*>(a.gate));
-        if (a.gate_kind == kGateToken) gs = __ldg(static_cast<const float*>(a.gate) + t);
-        float c2 = 0.0f, c1 = 0.0f, tok = 0.0f;
-        if (a.dh != nullptr) {
-            float unused = 0.0f;
-            for (int v = threadIdx.x; v < nvec; v += NT) {
-                float dh[E], x[E], g[E];
-                rn_load<false, E>(a.dh, row0 + v, dh);
-                rn_load<kBf16X, E>(a.x, row0 + v, x);
-#pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = 1.0f;
-                if (a.g_pre != nullptr) rn_load_gain<E>(a.g_pre, v, g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float u = x[e] * r2;
-                    c2 = fmaf(g[e] * dh[e], u, c2);
-                    if (a.part_pre != nullptr) acc_pre[v * E + e] = fmaf(dh[e], u, acc_pre[v * E + e]);
-                }
-            }
-            rn_block_sum2<NT>(c2, unused, red[0]);
-            c2 /= K;
-        }
-        // the gradient d of the new residual at vector v, and what follows from it: n, dn
-        auto at = [&](int v, float (&d)[E], float (&u1)[E], float (&n)[E], float (&dn)[E]) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = 0.0f;
-            if (a.dx != nullptr) rn_load<false, E>(a.dx, row0 + v, d);
-            if (a.dh != nullptr) {
-                float dh[E], x[E], g[E];
-                rn_load<false, E>(a.dh, row0 + v, dh);
-                rn_load<kBf16X, E>(a.x, row0 + v, x);
-#pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = 1.0f;
-                if (a.g_pre != nullptr) rn_load_gain<E>(a.g_pre, v, g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[e] += r2 * (g[e] * dh[e] - x[e] * r2 * c2);
-            }
-            float g[E];
-            rn_load<kBf16Y, E>(a.y, row0 + v, u1);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (a.post) u1[e] *= r1;
-                n[e] = u1[e];
-            }
-            if (a.g_post != nullptr) {
-                rn_load_gain<E>(a.g_post, v, g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) n[e] *= g[e];
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = gs;
-            if (a.gate_kind == kGateChannel) rn_load_gain<E>(static_cast<const float*>(a.gate), v, g);
-            if (a.gate_kind == kGateElement) rn_load<kBf16Y, E>(a.gate, row0 + v, g);
-#pragma unroll
-            for (int e = 0; e < E; ++e) dn[e] = a.beta * d[e] * g[e];
-        };
-        if (a.post || a.gate_kind != kGateNone) {
-            for (int v = threadIdx.x; v < nvec; v += NT) {
-                float d[E], u1[E], n[E], dn[E], g[E];
-                at(v, d, u1, n, dn);
-#pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = 1.0f;
-                if (a.g_post != nullptr) rn_load_gain<E>(a.g_post, v, g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float pn = a.beta * d[e] * n[e];
-                    tok += pn;
-                    if (a.part_gate != nullptr) acc_gate[v * E + e] += pn;
-                    c1 = fmaf(g[e] * dn[e], u1[e], c1);
-                    if (a.part_post != nullptr) acc_post[v * E + e] = fmaf(dn[e], u1[e], acc_post[v * E + e]);
-                }
-            }
-            scalar += static_cast<double>(tok);
-            rn_block_sum2<NT>(c1, tok, red[1]);
-            c1 /= K;
-            if (a.gate_kind == kGateToken && a.dgate != nullptr && threadIdx.x == 0)
-                static_cast<float*>(a.dgate)[t] = tok;
-        }
-        for (int v = threadIdx.x; v < nvec; v += NT) {
-            float d[E], u1[E], n[E], dn[E], g[E];
-            at(v, d, u1, n, dn);
-#pragma unroll
-            for (int e = 0; e < E; ++e) g[e] = 1.0f;
-            if (a.g_post != nullptr) rn_load_gain<E>(a.g_post, v, g);
-            if (a.gate_kind == kGateElement && a.dgate != nullptr) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) n[e] *= a.beta * d[e];
-                rn_store<kBf16Y, E>(a.dgate, row0 + v, n);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                d[e] *= a.alpha;
-                if (a.post) dn[e] = r1 * (g[e] * dn[e] - u1[e] * c1);
-            }
-            rn_store<false, E>(a.dX, row0 + v, d);
-            rn_store<kBf16Y, E>(a.dY, row0 + v, dn);
-        }
-        __syncthreads();                          // the sums in red[] are read before the next row's
-    }
-    for (int v = threadIdx.x; v < nvec; v += NT)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int64_t k = static_cast<int64_t>(v) * E + e, o = static_cast<int64_t>(blockIdx.x) * a.K + k;
-            if (a.part_pre != nullptr) a.part_pre[o] = acc_pre[k];
-            if (a.part_post != nullptr) a.part_post[o] = acc_post[k];
-            if (a.part_gate != nullptr) a.part_gate[o] = acc_gate[k];
-        }
-    if (a.part_scalar != nullptr) {
-        const double s = warp_sum(scalar);
-        if ((threadIdx.x & 31) == 0) red_s[threadIdx.x >> 5] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            double tot = 0.0;
-            for (int w = 0; w < NT / 32; ++w) tot += red_s[w];
-            a.part_scalar[blockIdx.x] = tot;
-        }
-    }
+// Two sums over the threads of a group, or of a whole cluster, with one barrier.  In a cluster
+// every warp sends its sums to every block's slots (8 bytes of distributed shared memory that
+// count on that block's mbarrier), so one wait stands for the block barrier and the exchange.
+// Slots alternate by row: a block sends row i + 2 only after all warps of all blocks have sent
+// row i + 1, hence read row i's slots.
+__device__ __forceinline__ void rn_add2(float2& v, int o) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+}
+__device__ __forceinline__ void st_async_v2(uint32_t addr, uint32_t bar, float2 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "f"(v.x), "f"(v.y), "r"(bar)
+                 : "memory");
 }
 
-// The same through a ring of rows (see the forward): thread i of a group owns vectors of four
-// columns i + j * TG, j < EPT / 4, of every row its group takes, and keeps their column sums in
-// registers.  A row is read from shared memory twice (c2 first, then everything else); what the
-// last pass needs, e1 (dn without the post norm) and u1, stays in registers, so the stage is
-// refilled before it.  At the end the groups' sums are joined in shared memory in group order and
-// the block writes one partial row for each.
-template <bool kBf16X, bool kBf16Y, int TG, int kMaxThreads, int EPT, bool kSm>
-__global__ void __launch_bounds__(kMaxThreads, 1)
-    residual_norm_bwd_ring_kernel(const RnBwdArgs a, int stages, uint64_t wait_ns) {
-    constexpr int VPT = EPT / 4;
-    constexpr int kRG = kMaxThreads / TG;
+// Through a ring of rows (see the forward): thread i of a group owns vectors i + j * TG of four
+// columns (kOdd: one), EPT columns in all, of every row its group takes, and keeps their column sums
+// in registers.  A row is read from shared memory twice (for c2, then for everything else);
+// what the last pass needs, w d and u1, stays in registers, so the stage is refilled before it.
+// The first pass of the next row runs before the barrier that ends the second pass of this one, so
+// a row costs one barrier: its reduction carries this row's sum of w q and c2 of the next.
+// kCl > 1: a cluster of kCl blocks shares each row, cols columns a block, so that gains and two
+// stages always fit.  At the end the groups' sums are joined in shared memory in group order and
+// each block (or cluster) writes one partial row.
+template <bool kBf16X, bool kBf16Y, int TG, int EPT, int kCl, bool kElem, bool kOdd>
+__global__ void __launch_bounds__(512, 1)
+    residual_norm_bwd_ring_kernel(const RnBwdArgs a, int cols, int stages, uint64_t wait_ns) {
+    constexpr int kThreads = 512;
+    constexpr int E = kOdd ? 1 : 4;
+    constexpr int VPT = EPT / E;
+    constexpr int kRG = kThreads / TG;
+    constexpr int kW = TG / 32 * kCl;                 // warps that join a row's sums
+    static_assert(kCl == 1 || TG == kThreads, "a cluster's blocks are one group each");
     extern __shared__ __align__(128) uint8_t rn_smem[];
     __shared__ uint64_t full[kRG][kRnMaxStages];
-    __shared__ float red_2[kRG][2][TG / 32], red_1[kRG][2][TG / 32], red_t[kRG][2][TG / 32];
-    __shared__ double red_s[kMaxThreads / 32];
+    __shared__ uint64_t xbar[2];
+    __shared__ __align__(16) float2 red[kRG][2][kW];
+    __shared__ double red_s[kThreads / 32];
     __shared__ int abort_flag;
-    const int g = threadIdx.x / TG, tid = threadIdx.x % TG;
+    const int g = threadIdx.x / TG, tid = threadIdx.x % TG, lane = threadIdx.x & 31;
     const int RG = blockDim.x / TG;
-    if (threadIdx.x == 0) abort_flag = 0;
+    const int rank = kCl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        mbar_init(&xbar[0], 1);
+        mbar_init(&xbar[1], 1);
+    }
     if (tid == 0) {
         for (int s = 0; s < stages; ++s) mbar_init(&full[g][s], 1);
         fence_mbar_init();
     }
-    __syncthreads();
+    if constexpr (kCl > 1) cluster_sync_all();
+    else __syncthreads();
     pdl_trigger_and_wait();
 
-    const int nvec = a.K / 4;
-    const bool has_dx = a.dx != nullptr, has_dh = a.dh != nullptr, elem = a.gate_kind == kGateElement;
+    // this block's columns [k0, k0 + cols)
+    const int k0 = rank * cols;
+    cols = min(cols, a.K - k0);
+    const int nvec = cols / E, v0 = k0 / E;
+    const int64_t row_vecs = a.K / E;
+    const bool has_dx = a.dx != nullptr, has_dh = a.dh != nullptr;
     // a row's arrays in its stage: dx, dh, x, y, gate
-    const uint32_t fb = a.K * 4u, xb = a.K * (kBf16X ? 2u : 4u), yb = a.K * (kBf16Y ? 2u : 4u);
-    const uint32_t o_dh = has_dx ? fb : 0u, o_x = o_dh + (has_dh ? fb : 0u), o_y = o_x + (has_dh ? xb : 0u), o_g = o_y + yb;
-    const uint32_t row_bytes = o_g + (elem ? yb : 0u);
+    constexpr int xs = kBf16X ? 2 : 4, ys = kBf16Y ? 2 : 4;
+    const uint32_t fb = cols * 4u, xb = cols * xs, yb = cols * ys;
+    const uint32_t pf = rn_pitch(kOdd, fb), px = rn_pitch(kOdd, xb), py = rn_pitch(kOdd, yb);
+    const uint32_t o_dh = has_dx ? pf : 0u, o_x = o_dh + (has_dh ? pf : 0u), o_y = o_x + (has_dh ? px : 0u), o_g = o_y + py;
+    const uint32_t row_bytes = o_g + (kElem ? py : 0u);
+    const uint32_t gain_bytes = (fb + 15u) & ~15u;
     float* g2_sm = reinterpret_cast<float*>(rn_smem);
-    float* g1_sm = g2_sm + a.K;
-    float* gt_sm = g1_sm + a.K;
-    uint8_t* ring = rn_smem + (kSm ? static_cast<size_t>(a.K) * 12 : 0) + static_cast<size_t>(g) * stages * row_bytes;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * RG;
+    float* w_sm = reinterpret_cast<float*>(rn_smem + gain_bytes);
+    uint8_t* ring = rn_smem + 2 * gain_bytes + static_cast<size_t>(g) * stages * row_bytes;
+    const int64_t step = static_cast<int64_t>(gridDim.x / kCl) * RG;
     auto issue = [&](int64_t t, int s) {
         uint8_t* dst = ring + static_cast<size_t>(s) * row_bytes;
         uint64_t* bar = &full[g][s];
-        mbar_arrive_expect_tx(bar, row_bytes);
-        if (has_dx) bulk_load(dst, reinterpret_cast<const uint8_t*>(a.dx) + t * fb, fb, bar);
-        if (has_dh) {
-            bulk_load(dst + o_dh, reinterpret_cast<const uint8_t*>(a.dh) + t * fb, fb, bar);
-            bulk_load(dst + o_x, static_cast<const uint8_t*>(a.x) + t * xb, xb, bar);
+        const int64_t at = t * a.K + k0;
+        const uint8_t *dxg = reinterpret_cast<const uint8_t*>(a.dx), *dhg = reinterpret_cast<const uint8_t*>(a.dh),
+                      *xg = static_cast<const uint8_t*>(a.x), *yg = static_cast<const uint8_t*>(a.y),
+                      *gg = static_cast<const uint8_t*>(a.gate);
+        if constexpr (kOdd) {
+            const int64_t all = static_cast<int64_t>(a.T) * a.K;
+            RnSpan s1{0, 0}, s2{0, 0}, s3{0, 0}, s5{0, 0};
+            if (has_dx) s1 = rn_span<4>(dst, dxg, at * 4, at * 4 + fb, all * 4);
+            if (has_dh) {
+                s2 = rn_span<4>(dst + o_dh, dhg, at * 4, at * 4 + fb, all * 4);
+                s3 = rn_span<xs>(dst + o_x, xg, at * xs, at * xs + xb, all * xs);
+            }
+            const RnSpan s4 = rn_span<ys>(dst + o_y, yg, at * ys, at * ys + yb, all * ys);
+            if constexpr (kElem) s5 = rn_span<ys>(dst + o_g, gg, at * ys, at * ys + yb, all * ys);
+            mbar_arrive_expect_tx(bar, s1.n + s2.n + s3.n + s4.n + s5.n);
+            if (s1.n) bulk_load(dst, dxg + s1.lo, s1.n, bar);
+            if (s2.n) bulk_load(dst + o_dh, dhg + s2.lo, s2.n, bar);
+            if (s3.n) bulk_load(dst + o_x, xg + s3.lo, s3.n, bar);
+            if (s4.n) bulk_load(dst + o_y, yg + s4.lo, s4.n, bar);
+            if (s5.n) bulk_load(dst + o_g, gg + s5.lo, s5.n, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, row_bytes);
+            if (has_dx) bulk_load(dst, dxg + at * 4, fb, bar);
+            if (has_dh) {
+                bulk_load(dst + o_dh, dhg + at * 4, fb, bar);
+                bulk_load(dst + o_x, xg + at * xs, xb, bar);
+            }
+            bulk_load(dst + o_y, yg + at * ys, yb, bar);
+            if constexpr (kElem) bulk_load(dst + o_g, gg + at * ys, yb, bar);
         }
-        bulk_load(dst + o_y, static_cast<const uint8_t*>(a.y) + t * yb, yb, bar);
-        if (elem) bulk_load(dst + o_g, static_cast<const uint8_t*>(a.gate) + t * yb, yb, bar);
     };
-    const int64_t t_first = static_cast<int64_t>(blockIdx.x) * RG + g;
+    // byte offsets of row t's elements behind those of the arrays in a stage
+    auto shift = [&](int64_t t, int size) -> uint32_t { return kOdd ? rn_shift((t * a.K + k0) * size) : 0u; };
+    const int64_t t_first = static_cast<int64_t>(blockIdx.x / kCl) * RG + g;
     if (tid == 0)
         for (int s = 0; s < stages; ++s)
             if (t_first + s * step < a.T) issue(t_first + s * step, s);
 
-    auto ones = [](float (&f)[4]) { f[0] = f[1] = f[2] = f[3] = 1.0f; };
-    if constexpr (kSm) {
-        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
-            float f[4];
-            ones(f);
-            if (a.g_pre != nullptr) rn_load_gain<4>(a.g_pre, v, f);
-            rn_gain_put<4>(g2_sm, v, nvec, f);
-            ones(f);
-            if (a.g_post != nullptr) rn_load_gain<4>(a.g_post, v, f);
-            rn_gain_put<4>(g1_sm, v, nvec, f);
-            ones(f);
-            if (a.gate_kind == kGateChannel) rn_load_gain<4>(static_cast<const float*>(a.gate), v, f);
-            rn_gain_put<4>(gt_sm, v, nvec, f);
-        }
-        __syncthreads();
+    for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+        float f[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = 1.0f;
+        if (a.g_pre != nullptr) rn_load_gain<E>(a.g_pre, v0 + v, f);
+        rn_gain_put<E>(g2_sm, v, nvec, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = rn_col_w(a, k0 + E * v + e);
+        rn_gain_put<E>(w_sm, v, nvec, f);
     }
-    auto gain = [&](const float* sm, const float* gm, bool have, int v, float (&f)[4]) {
-        if constexpr (kSm) {
-            rn_gain<true, 4>(sm, v, nvec, f);
-        } else {
-            ones(f);
-            if (have) rn_load_gain<4>(gm, v, f);
-        }
-    };
+    __syncthreads();
 
-    float acc_pre[VPT][4], acc_post[VPT][4], acc_gate[VPT][4];
+    float acc_pre[VPT][E], acc_s[VPT][E];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc_pre[j][e] = acc_post[j][e] = acc_gate[j][e] = 0.0f;
+        for (int e = 0; e < E; ++e) acc_pre[j][e] = acc_s[j][e] = 0.0f;
     const float invK = 1.0f / static_cast<float>(a.K);
-    const bool want_tok = a.gate_kind == kGateToken && a.dgate != nullptr;
-    double scalar = 0.0;
-    float gs = 1.0f;
-    if (a.gate_kind == kGateScalar) gs = __ldg(static_cast<const float*>(a.gate));
+
+    uint32_t par = 0, xph = 0;
+    auto reduce = [&](float2 v) -> float2 {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) rn_add2(v, o);
+        if constexpr (kCl == 1) {
+            if constexpr (TG == 32) {
+                __syncwarp();
+                return v;
+            }
+            if (lane == 0) red[g][par][tid >> 5] = v;
+            rn_group_sync<TG>(g);
+        } else {
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(&xbar[par], kW * 8u);
+            if (lane < kCl)
+                st_async_v2(mapa_shared(smem_u32(&red[0][par][rank * (TG / 32) + (tid >> 5)]), lane),
+                            mapa_shared(smem_u32(&xbar[par]), lane), v);
+            mbar_wait(&xbar[par], xph, wait_ns, &abort_flag);
+        }
+        v = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < (kW + 31) / 32; ++i) {
+            const float2 w = red[g][par][(lane & (kW - 1)) + 32 * i];
+            v.x += w.x;
+            v.y += w.y;
+        }
+#pragma unroll
+        for (int o = (kW < 32 ? kW : 32) / 2; o > 0; o >>= 1) rn_add2(v, o);
+        if (par) xph ^= 1u;
+        par ^= 1u;
+        return v;
+    };
+    // this thread's part of sum_k g2 dh x, and the column sums of dh u2, of row t in stage s
+    auto first_pass = [&](int64_t t, int s, float r2) -> float {
+        const uint8_t* row = ring + static_cast<size_t>(s) * row_bytes;
+        const uint8_t *dh_r = row + o_dh + shift(t, 4), *x_r = row + o_x + shift(t, xs);
+        float c2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = tid + j * TG;
+            if (v >= nvec) continue;
+            float dh[E], x[E], q[E];
+            rn_lds<false, E>(dh_r, v, dh);
+            rn_lds<kBf16X, E>(x_r, v, x);
+            rn_gain<true, E>(g2_sm, v, nvec, q);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float z = dh[e] * x[e];
+                c2 = fmaf(z, q[e], c2);
+                acc_pre[j][e] = fmaf(z, r2, acc_pre[j][e]);
+            }
+        }
+        return c2;
+    };
 
     int s = 0;
-    uint32_t ph = 0, par = 0;
-    for (int64_t t = t_first; t < a.T; t += step, par ^= 1u) {
-        const float r2 = has_dh ? __ldg(a.r_pre + t) : 0.0f;
+    uint32_t ph = 0;
+    float r2 = 0.0f, c2 = 0.0f;
+    if (t_first < a.T && has_dh) {
+        r2 = __ldg(a.r_pre + t_first);
+        mbar_wait(&full[g][0], 0, wait_ns, &abort_flag);
+        c2 = reduce(make_float2(0.0f, first_pass(t_first, 0, r2))).y * invK;
+    }
+    for (int64_t t = t_first; t < a.T; t += step) {
         const float r1 = a.post ? __ldg(a.r_post + t) : 1.0f;
-        if (a.gate_kind == kGateToken) gs = __ldg(static_cast<const float*>(a.gate) + t);
-        mbar_wait(&full[g][s], ph, wait_ns, &abort_flag);
+        const float f = a.gate_kind == kGateToken ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
+        const bool more = has_dh && t + step < a.T;
+        const float r2n = more ? __ldg(a.r_pre + t + step) : 0.0f;
+        if (!has_dh) mbar_wait(&full[g][s], ph, wait_ns, &abort_flag);
         const uint8_t* row = ring + static_cast<size_t>(s) * row_bytes;
-        const int64_t row0 = t * nvec;
-        float c2 = 0.0f;
-        if (has_dh) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int v = tid + j * TG;
-                if (v >= nvec) continue;
-                float dh[4], x[4], q[4];
-                rn_lds<false, 4>(row + o_dh, v, dh);
-                rn_lds<kBf16X, 4>(row + o_x, v, x);
-                gain(g2_sm, a.g_pre, a.g_pre != nullptr, v, q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float u = x[e] * r2;
-                    c2 = fmaf(q[e] * dh[e], u, c2);
-                    acc_pre[j][e] = fmaf(dh[e], u, acc_pre[j][e]);
-                }
-            }
-            c2 = rn_group_reduce<TG>(c2, red_2[g][par], g, [](float p, float q) { return p + q; }) * invK;
-        }
-        const float b2 = -r2 * c2;                // d = dx + r2 (e - u2 c2)
-        float e1[VPT][4], u1[VPT][4];
-        float c1 = 0.0f, tok = 0.0f;
+        const uint8_t *dx_r = row + shift(t, 4), *dh_r = dx_r + o_dh, *x_r = row + o_x + shift(t, xs),
+                      *y_r = row + o_y + shift(t, ys);
+        const int64_t row0 = t * row_vecs + v0;
+        const float b2 = -r2 * r2 * r2 * c2;      // d = dx + r2 g2 dh + x b2
+        float wd[VPT][E], u1[VPT][E];
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * TG;
             if (v >= nvec) continue;
-            float d[4], q[4], gt[4];
+            float d[E], w[E];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = 0.0f;
-            if (has_dx) rn_lds<false, 4>(row, v, d);
+            for (int e = 0; e < E; ++e) d[e] = 0.0f;
+            if (has_dx) rn_lds<false, E>(dx_r, v, d);
             if (has_dh) {
-                float dh[4], x[4];
-                rn_lds<false, 4>(row + o_dh, v, dh);
-                rn_lds<kBf16X, 4>(row + o_x, v, x);
-                gain(g2_sm, a.g_pre, a.g_pre != nullptr, v, q);
+                float dh[E], x[E], g2[E];
+                rn_lds<false, E>(dh_r, v, dh);
+                rn_lds<kBf16X, E>(x_r, v, x);
+                rn_gain<true, E>(g2_sm, v, nvec, g2);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = fmaf(r2, fmaf(x[e], b2, q[e] * dh[e]), d[e]);
+                for (int e = 0; e < E; ++e) d[e] = fmaf(x[e], b2, fmaf(g2[e] * dh[e], r2, d[e]));
             }
-            rn_lds<kBf16Y, 4>(row + o_y, v, u1[j]);
-            gain(g1_sm, a.g_post, a.g_post != nullptr, v, q);
-            if (elem) {
-                rn_lds<kBf16Y, 4>(row + o_g, v, gt);
-            } else if (a.gate_kind == kGateChannel) {
-                gain(gt_sm, static_cast<const float*>(a.gate), true, v, gt);
+            rn_lds<kBf16Y, E>(y_r, v, u1[j]);
+            rn_gain<true, E>(w_sm, v, nvec, w);
+            if constexpr (kElem) {
+                float gt[E], dg[E];
+                rn_lds<kBf16Y, E>(y_r + (o_g - o_y), v, gt);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    u1[j][e] *= r1;
+                    const float q = d[e] * u1[j][e];
+                    dg[e] = w[e] * q;
+                    acc_s[j][e] = fmaf(gt[e], q, acc_s[j][e]);
+                    wd[j][e] = gt[e] * (w[e] * d[e]);
+                    sum.x = fmaf(gt[e], dg[e], sum.x);
+                }
+                if (a.dgate != nullptr) rn_store<kBf16Y, E>(a.dgate, row0 + v, dg);
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) gt[e] = gs;
+                for (int e = 0; e < E; ++e) {
+                    u1[j][e] *= r1;
+                    const float q = d[e] * u1[j][e];
+                    acc_s[j][e] = fmaf(f, q, acc_s[j][e]);
+                    wd[j][e] = w[e] * d[e];
+                    sum.x = fmaf(w[e], q, sum.x);
+                }
             }
-            float dg[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                u1[j][e] *= r1;
-                const float p = a.beta * d[e];
-                dg[e] = p * (u1[j][e] * q[e]);
-                tok += dg[e];
-                acc_gate[j][e] += dg[e];
-                const float dn = p * gt[e];
-                acc_post[j][e] = fmaf(dn, u1[j][e], acc_post[j][e]);
-                e1[j][e] = q[e] * dn;
-                c1 = fmaf(e1[j][e], u1[j][e], c1);
-                d[e] *= a.alpha;
-            }
-            rn_store<false, 4>(a.dX, row0 + v, d);
-            if (elem && a.dgate != nullptr) rn_store<kBf16Y, 4>(a.dgate, row0 + v, dg);
+            for (int e = 0; e < E; ++e) d[e] *= a.alpha;
+            rn_store<false, E>(a.dX, row0 + v, d);
         }
-        scalar += static_cast<double>(tok);
-        if (a.post) c1 = rn_group_reduce<TG>(c1, red_1[g][par], g, [](float p, float q) { return p + q; }) * invK;
-        if (want_tok) {
-            tok = rn_group_reduce<TG>(tok, red_t[g][par], g, [](float p, float q) { return p + q; });
-            if (tid == 0) static_cast<float*>(a.dgate)[t] = tok;
-        }
-        if (TG == 32 || (!a.post && !want_tok)) rn_group_sync<TG>(g);
-        // every thread of the group has read the stage
-        if (tid == 0 && t + stages * step < a.T) issue(t + stages * step, s);
+        const int s_row = s;
         if (++s == stages) { s = 0; ph ^= 1u; }
+        if (more) {
+            mbar_wait(&full[g][s], ph, wait_ns, &abort_flag);
+            sum.y = first_pass(t + step, s, r2n);
+        }
+        sum = reduce(sum);
+        // every thread of the group has read the stage
+        if (tid == 0 && t + stages * step < a.T) issue(t + stages * step, s_row);
+        r2 = r2n;
+        c2 = sum.y * invK;
+        if (tid == 0 && rank == 0 && a.gate_kind == kGateToken && a.dgate != nullptr)
+            static_cast<float*>(a.dgate)[t] = sum.x;
+        const float c1 = -sum.x * invK, fr = f * r1;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = tid + j * TG;
             if (v >= nvec) continue;
-            if (a.post) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) e1[j][e] = r1 * fmaf(-u1[j][e], c1, e1[j][e]);
-            }
-            rn_store<kBf16Y, 4>(a.dY, row0 + v, e1[j]);
+            for (int e = 0; e < E; ++e) wd[j][e] = fr * (a.post ? fmaf(u1[j][e], c1, wd[j][e]) : wd[j][e]);
+            rn_store<kBf16Y, E>(a.dY, row0 + v, wd[j]);
         }
     }
     if (tid == 0 && abort_flag != 0) {
@@ -949,75 +945,114 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             if (++s == stages) { s = 0; ph ^= 1u; }
         }
     }
-    if (a.part_scalar != nullptr) {
-        const double w = warp_sum(scalar);
-        if ((threadIdx.x & 31) == 0) red_s[threadIdx.x >> 5] = w;
-    }
     __syncthreads();                              // every group is through its rows and its loads
-    if (a.part_scalar != nullptr && threadIdx.x == 0) {
-        double tot = 0.0;
-        for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) tot += red_s[w];
-        a.part_scalar[blockIdx.x] = tot;
-    }
-    if (a.part_pre == nullptr && a.part_post == nullptr && a.part_gate == nullptr) return;
-    float* sums = reinterpret_cast<float*>(rn_smem);   // [group][3][K]
-    float* mine = sums + static_cast<size_t>(g) * 3 * a.K;
+    if (a.part_pre != nullptr || a.part_s != nullptr || a.part_scalar != nullptr) {
+        float* sums = reinterpret_cast<float*>(rn_smem);   // [group][2][cols]
+        float* mine = sums + static_cast<size_t>(g) * 2 * cols;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = tid + j * TG;
-        if (v >= nvec) continue;
-        rn_gain_put<4>(mine, v, nvec, acc_pre[j]);
-        rn_gain_put<4>(mine + a.K, v, nvec, acc_post[j]);
-        rn_gain_put<4>(mine + 2 * a.K, v, nvec, acc_gate[j]);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 3 * nvec; i += blockDim.x) {
-        const int which = i / nvec, v = i - which * nvec;
-        float* part = which == 0 ? a.part_pre : which == 1 ? a.part_post : a.part_gate;
-        if (part == nullptr) continue;
-        float4 tot = reinterpret_cast<const float4*>(sums + static_cast<size_t>(which) * a.K)[v];
-        for (int q = 1; q < RG; ++q) {
-            const float4 w = reinterpret_cast<const float4*>(sums + static_cast<size_t>(q * 3 + which) * a.K)[v];
-            tot.x += w.x; tot.y += w.y; tot.z += w.z; tot.w += w.w;
+        for (int j = 0; j < VPT; ++j) {
+            const int v = tid + j * TG;
+            if (v >= nvec) continue;
+            rn_gain_put<E>(mine, v, nvec, acc_pre[j]);
+            rn_gain_put<E>(mine + cols, v, nvec, acc_s[j]);
         }
-        reinterpret_cast<float4*>(part + static_cast<int64_t>(blockIdx.x) * a.K)[v] = tot;
+        __syncthreads();
+        double scalar = 0.0;
+        const int64_t out0 = static_cast<int64_t>(blockIdx.x / kCl) * a.K + k0;
+        for (int i = threadIdx.x; i < 2 * nvec; i += blockDim.x) {
+            const int which = i >= nvec, v = i - which * nvec;
+            float tot[E];
+            rn_gain<true, E>(sums + static_cast<size_t>(which) * cols, v, nvec, tot);
+            for (int q = 1; q < RG; ++q) {
+                float w[E];
+                rn_gain<true, E>(sums + static_cast<size_t>(q * 2 + which) * cols, v, nvec, w);
+#pragma unroll
+                for (int e = 0; e < E; ++e) tot[e] += w[e];
+            }
+            float* part = which ? a.part_s : a.part_pre;
+            if (part != nullptr) rn_store<false, E>(part + out0, v, tot);
+            if (which && a.part_scalar != nullptr) {
+                float q[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) q[e] = 1.0f;
+                if (a.g_post != nullptr) rn_load_gain<E>(a.g_post, v0 + v, q);
+#pragma unroll
+                for (int e = 0; e < E; ++e) scalar += static_cast<double>(q[e] * tot[e]);
+            }
+        }
+        if (a.part_scalar != nullptr) {
+            scalar = warp_sum(scalar);
+            if (lane == 0) red_s[threadIdx.x >> 5] = scalar;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                double tot = 0.0;
+                for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) tot += red_s[w];
+                a.part_scalar[blockIdx.x] = tot;
+            }
+        }
+    }
+    if constexpr (kCl > 1) {
+        __syncwarp();
+        cluster_sync_all();                       // no block leaves while another may send to it
     }
 }
 
-// The column sums' partials [G x K], added in block order: blockIdx.y picks the gradient
-// (dg2, dg1, channel gate), a block takes 32 columns with 32 warps (lane = column, warp w adds
-// partial rows w, w + 32, ..., then warp 0 adds the warps).  The scalar gate's partials are
-// added by the first block of the third.
+// The column sums' partials [G x K], added in block order.  blockIdx.y = 0: dg2; 1: S, which gives
+// dg1 = beta gate S and a channel gate's beta g1 S.  A block takes 32 columns with 32 warps (lane =
+// column, warp w adds partial rows w, w + 32, ..., then warp 0 adds the warps).  A scalar gate's
+// partials are added by the first block.
 struct RnReduceArgs {
-    const float* part[3];
-    float* out[3];
+    const float* part_pre;
+    const float* part_s;
     const double* part_scalar;
-    float* dscalar;
-    int G, K;
+    const float* gate;     // channel or scalar gate, or NULL (the sums hold it)
+    const float* g_post;
+    float* dg_pre;
+    float* dg_post;
+    float* dgate;          // channel [K] or scalar [1], or NULL
+    float beta;
+    int gate_kind;
+    int G, Gs, K;          // partial rows, scalar partials
 };
 __global__ void __launch_bounds__(1024) rn_reduce_kernel(const RnReduceArgs a) {
     __shared__ float red[32][33];
     pdl_trigger_and_wait();
     const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
-    if (blockIdx.y == 2 && blockIdx.x == 0 && a.part_scalar != nullptr && w == 0) {
+    if (blockIdx.y == 1 && blockIdx.x == 0 && a.part_scalar != nullptr && w == 0) {
         double s = 0.0;
-        for (int p = c; p < a.G; p += 32) s += a.part_scalar[p];
+        for (int p = c; p < a.Gs; p += 32) s += a.part_scalar[p];
         s = warp_sum(s);
-        if (c == 0) *a.dscalar = static_cast<float>(s);
+        if (c == 0) *a.dgate = static_cast<float>(static_cast<double>(a.beta) * s);
     }
-    const float* part = a.part[blockIdx.y];
+    const float* part = blockIdx.y ? a.part_s : a.part_pre;
     if (part == nullptr) return;
     const int k = blockIdx.x * 32 + c;
+    float v[(kRnMaxBlocks + 31) / 32];
+#pragma unroll
+    for (int i = 0; i < (kRnMaxBlocks + 31) / 32; ++i) {
+        const int p = w + 32 * i;
+        v[i] = (k < a.K && p < a.G) ? __ldcs(part + static_cast<int64_t>(p) * a.K + k) : 0.0f;
+    }
     float s = 0.0f;
-    for (int p = w; p < a.G; p += 32) s += k < a.K ? __ldcs(part + static_cast<int64_t>(p) * a.K + k) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < (kRnMaxBlocks + 31) / 32; ++i) s += v[i];
     red[w][c] = s;
     __syncthreads();
-    if (w == 0 && k < a.K) {
-        float tot = 0.0f;
+    if (w != 0 || k >= a.K) return;
+    float tot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) tot += red[i][c];
-        a.out[blockIdx.y][k] = tot;
+    for (int i = 0; i < 32; ++i) tot += red[i][c];
+    if (blockIdx.y == 0) {
+        a.dg_pre[k] = tot;
+        return;
     }
+    tot *= a.beta;
+    if (a.dg_post != nullptr)
+        a.dg_post[k] = a.gate_kind == kGateChannel  ? tot * __ldg(a.gate + k)
+                       : a.gate_kind == kGateScalar ? tot * __ldg(a.gate)
+                                                    : tot;
+    if (a.dgate != nullptr && a.gate_kind == kGateChannel)
+        a.dgate[k] = a.g_post != nullptr ? tot * __ldg(a.g_post + k) : tot;
 }
 
 }  // namespace bl

@@ -12,6 +12,9 @@ DEV = "cuda:0"
 F, B = torch.float32, torch.bfloat16
 TYPES = [(F, F), (B, B), (F, B)]
 GATES = ["none", "scalar", "channel", "token", "element"]
+# rows enough for the forward's shared-memory ring, whole vectors and odd ones, in every group size
+RING = [(6200, 256), (3100, 512), (1600, 1000), (800, 2048), (420, 4096), (200, 8192), (150, 11008), (100, 16384),
+        (3400, 500), (3601, 499), (1601, 1001), (500, 4001), (200, 8191), (130, 12289), (100, 16381)]
 # warp rows, block rows of every block size, and rows that are no whole vectors
 SIZES = [(1, 1), (3, 7), (5, 8), (9, 33), (2, 96), (40, 250), (17, 256), (300, 512), (77, 1003), (6, 1024), (1, 2048),
          (13, 4096), (4, 5000), (3, 5001), (5, 11008), (2, 16384), (2, 16381)]
@@ -65,6 +68,15 @@ def test_forward_sizes(bl, T, K, i):
     xt, yt = TYPES[i]
     mode = ["quant" if K % 32 == 0 else "norm", "norm", "none"][(T + i) % 3]
     check_forward(bl, T, K, xt, yt, GATES[(T + K + i) % 5], (T + i) % 4 != 0, (K + i) % 3 != 0, mode)
+
+
+@pytest.mark.parametrize("T,K", RING)
+@pytest.mark.parametrize("i", range(3))
+def test_forward_ring(bl, T, K, i):
+    xt, yt = TYPES[i]
+    for n, mode in enumerate(["quant", "norm", "none"] if K % 32 == 0 else ["norm", "norm", "none"]):
+        check_forward(bl, T, K, xt, yt, GATES[(T + i + n) % 5], (K // 8 + i + n) % 4 != 0, (T + i + n) % 3 != 0, mode)
+    check_backward(bl, T, K, xt, yt, GATES[(T + i) % 5], (K // 8 + i) % 4 != 0, True, True, True)
 
 
 @pytest.mark.parametrize("gate", GATES)
@@ -151,8 +163,7 @@ def test_backward_against_differences(bl, gate):
 
 def test_in_place(bl):
     """The new residual over the old one, and the gradient over either incoming one."""
-    T, K = 33, 1184
-    for xt, yt in TYPES:
+    for (T, K), (xt, yt) in [((33, 1184), t) for t in TYPES] + [((1400, 1184), t) for t in TYPES]:
         s = ref.inputs(T, K, xt, yt, "channel", 8, DEV)
         o = bl.bitlinear_residual_norm(**s, mode="quant")
         x = s["x"].clone()
@@ -204,7 +215,7 @@ def test_quantised_row_of_zeros(bl):
 
 def test_repeatable_and_rows_independent(bl):
     """The same bits again, and a row's results do not depend on the rows beside it."""
-    T, K = 600, 2048
+    T, K = 900, 2048                          # many rows through the ring, one row without it
     s = ref.inputs(T, K, F, B, "channel", 11, DEV)
     o = bl.bitlinear_residual_norm(**s)
     dx, dh = torch.randn(T, K, device=DEV), torch.randn(T, K, device=DEV)
@@ -222,7 +233,7 @@ def test_repeatable_and_rows_independent(bl):
 
 def test_nothing_outside_is_written(bl):
     """Outputs at the end of larger buffers: what lies behind them stays."""
-    for T, K in ((5, 72), (3, 1003), (2, 4096)):
+    for T, K in ((5, 72), (3, 1003), (2, 4096), (1700, 1001), (1600, 1000)):
         s = ref.inputs(T, K, F, F, "none", 12, DEV)
         pad = 64
         flat = {k: torch.full((T * K + pad,), 7.0, device=DEV) for k in ("x", "h", "dx", "dy")}
