@@ -7,6 +7,7 @@ to libbitlinear.so.  Every step of the computation runs in the library's kernels
 """
 from __future__ import annotations
 
+from array import array
 from typing import Optional
 
 import torch
@@ -476,31 +477,35 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
 # global gradient norm and clipping
 # ----------------------------------------------------------------------------------
 
+# unbound, to be mapped over lists of many tensors
+_T = torch.Tensor
+_t_numel, _t_ptr, _t_device, _t_dense, _t_dtype = (_T.numel, _T.data_ptr, _T.get_device, _T.is_contiguous,
+                                                   _T.dtype.__get__)
+
+
 def _grad_lists(grads, out):
-    """Device, and the host arrays that the entry points take: addresses, counts, types."""
-    n = len(grads)
-    if n == 0:
+    """Device, and host arrays of addresses, output addresses (or None), sizes and types."""
+    if len(grads) == 0:
         raise ValueError("grads must not be empty")
-    dev = grads[0].device
-    numel, types = [g.numel() for g in grads], [g.dtype for g in grads]
+    numel, types = list(map(_t_numel, grads)), list(map(_t_dtype, grads))
     every = grads
     if out is not None:
-        if [t.numel() for t in out] != numel or [t.dtype for t in out] != types:
+        if list(map(_t_numel, out)) != numel or list(map(_t_dtype, out)) != types:
             raise ValueError("out must have the sizes and types of grads")
         every = [*grads, *out]
-    where = dev.index
-    for t in every:
-        if t.get_device() != where or not t.is_contiguous():
-            raise ValueError(f"gradients and outputs must be contiguous CUDA tensors on one device, got {t.device}, "
-                             f"strides {t.stride()}")
+    where = set(map(_t_device, every))
+    if len(where) != 1 or -1 in where or not all(map(_t_dense, every)):
+        raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
     try:
-        codes = [_DT[t] for t in types]
+        codes = array("i", map(_DT.__getitem__, types))
     except KeyError as e:
         raise ValueError(f"unsupported dtype {e.args[0]}") from None
-    if where is None or where < 0:
-        raise ValueError("grads must be CUDA tensors")
-    return (dev, [g.data_ptr() for g in grads], None if out is None else [t.data_ptr() for t in out],
-            (_lib.I64 * n)(*numel), (_lib.INT * n)(*codes))
+    return (grads[0].device, array("q", map(_t_ptr, grads)), None if out is None else array("q", map(_t_ptr, out)),
+            array("q", numel), codes)
+
+
+def _at(a: array) -> int:
+    return a.buffer_info()[0]
 
 
 # the clip's workspace is the same for every list
@@ -530,8 +535,7 @@ def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tenso
     Returns dict(norm [1] f32, coef [1] f32); coef goes into bitlinear_optimizer_step."""
     dev, ptrs, _, numel, types = _grad_lists(grads, None)
     norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    n = len(ptrs)
-    _call(dev, "bitlinear_grad_norm", (_lib.P * n)(*ptrs), numel, types, n, max_norm, norm.data_ptr(), coef.data_ptr(),
+    _call(dev, "bitlinear_grad_norm", _at(ptrs), _at(numel), _at(types), len(ptrs), max_norm, norm.data_ptr(), coef.data_ptr(),
           ws.data_ptr(), ws.numel() * ws.element_size())
     return {"norm": norm, "coef": coef}
 
@@ -547,8 +551,7 @@ def bitlinear_clip_grads(grads, max_norm: float = 1.0, out=None, norm: Optional[
     if len(set(outs)) != n and len({p for p, k in zip(outs, numel) if k}) != sum(1 for k in numel if k):
         raise ValueError("a gradient is written twice")
     norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    arr = _lib.P * n
-    _call(dev, "bitlinear_clip_grads", arr(*ptrs), arr(*outs), numel, types, n, max_norm, norm.data_ptr(),
+    _call(dev, "bitlinear_clip_grads", _at(ptrs), _at(outs), _at(numel), _at(types), n, max_norm, norm.data_ptr(),
           coef.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return {"norm": norm, "coef": coef, "grads": grads if out is None else out}
 
