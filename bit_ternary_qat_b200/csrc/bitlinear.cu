@@ -378,7 +378,8 @@ bl_status run_linear(const int8_t* Xq, const float* sx, int64_t T, int64_t K, co
 }
 
 // Per-column scales gamma_n: the 2-SM kernel at every T (its rows past T are zero-filled
-// loads and clipped stores).
+// loads and clipped stores).  kInt8: the 8-bit linear's order of the two scales.
+template <bool kInt8 = false>
 bl_status run_linear_rows(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq,
                           const float* gamma_rows, int64_t N, void* Y, bl_dtype y_dt, int32_t* acc, cudaStream_t st,
                           const DeviceInfo& dev) {
@@ -390,10 +391,10 @@ bl_status run_linear_rows(const int8_t* Xq, const float* sx, int64_t T, int64_t 
     a.acc_out = acc; a.row_scale = sx; a.gamma = gamma_rows;
     if (y_dt == BL_BF16) {
         BL_TRY(make_tmap(&td, Y, kTmBf16, (uint64_t)N, (uint64_t)T, 64, 32));
-        return launch_tc2<true, false, false, bl::kEpiLinearColBf16>(ta, tb, td, a, st, dev);
+        return launch_tc2<true, false, false, kInt8 ? bl::kEpiInt8Bf16 : bl::kEpiLinearColBf16>(ta, tb, td, a, st, dev);
     }
     BL_TRY(make_tmap(&td, Y, kTmF32, (uint64_t)N, (uint64_t)T, 32, 32));
-    return launch_tc2<true, false, false, bl::kEpiLinearColF32>(ta, tb, td, a, st, dev);
+    return launch_tc2<true, false, false, kInt8 ? bl::kEpiInt8F32 : bl::kEpiLinearColF32>(ta, tb, td, a, st, dev);
 }
 
 bl_status run_grad_input_gemm(const void* dY, bl_dtype dt, const uint16_t* Wq_bf16, const float* gamma, int64_t T,
@@ -1208,7 +1209,7 @@ bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int6
 
 // |Xq|, |Wq| <= 128: a sum of K products stays below 2^31 for K < 2^17.
 constexpr int64_t kMaxInt8K = int64_t(1) << 17;
-constexpr int64_t kFewTokens = 256;
+constexpr int64_t kFewTokens = 192;
 
 }  // namespace
 
@@ -1889,12 +1890,15 @@ bl_status bitlinear_linear_int8(const int8_t* Xq, const float* sx, int64_t T, in
     DeviceInfo dev;
     BL_TRY(current_device(&dev));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T <= kFewTokens) {
+    // The few-token kernel up to 192 tokens, and up to one token tile (256) while the large tiles of
+    // 256 weight rows would fill less than half the pairs (256 tokens: 4096 x 4096 15.3 us against
+    // 21.6, 28672 x 8192 65.2 against 57.6)
+    if (T <= kFewTokens || (T <= bl::kI8MaxTokens && (N + 255) / 256 * 4 < dev.sms)) {
         if (y_dt == BL_BF16)
             return run_linear_int8_few<true>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
         return run_linear_int8_few<false>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
     }
-    return run_linear_rows(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, y_dt, acc, st, dev);
+    return run_linear_rows<true>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, y_dt, acc, st, dev);
 }
 
 bl_status bl_mma_peak_probe(int kind, int pair, int iters, double* ops_out, void* stream) {

@@ -1,6 +1,6 @@
 // gemm_int8.cuh -- the 8-bit linear for few tokens (single decoded tokens to a few hundred).
 //
-//   acc[t, n] = sum_k X_q[t, k] W_q[n, k]       y = fl(acc * fl(gamma_n / s_t))
+//   acc[t, n] = sum_k X_q[t, k] W_q[n, k]       y = fl( fl(acc gamma_n) r_t ),  r_t = fl(1 / s_t)
 //
 // With few tokens the product reads the weight once and is bound by HBM, so the tiles are cut
 // for the read, not for the tensor core: the weight rows are the M side of tcgen05.mma (kind::i8,
@@ -12,15 +12,18 @@
 // and the int32 partial sums are added through distributed shared memory (whole numbers: any
 // order gives the same sum).  No workspace, one launch.
 //
-// Roles as in gemm_tc.cuh: warp 0 TMA producer, warp 1 MMA issuer, warps 2..5 epilogue; every
-// mbarrier wait is bounded, and a block that gives up still reaches the cluster barriers.
+// Roles as in gemm_tc.cuh: warp 0 TMA producer, warp 1 MMA issuer, warps 2..9 epilogue (two to a
+// quadrant of TMEM lanes, taking 16 tokens in turn: with few rows a tile only some quadrants hold
+// rows, and with 256 tokens an epilogue of four warps that divided by s_t took longer than the
+// loads: 11008 x 4096, 41 us, 14 without it, 21 as it is).  Every mbarrier wait is bounded, and a
+// block that gives up still reaches the cluster barriers.
 #pragma once
 #include <cuda.h>
 #include "common.cuh"
 
 namespace bl {
 
-constexpr int kI8Threads = 192;
+constexpr int kI8Threads = 320;
 constexpr int kI8MaxStages = 24;
 constexpr int kI8MaxTokens = 256;      // token side of one tile
 
@@ -72,9 +75,8 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
 }
 
 template <bool kBf16Out>
-__device__ __forceinline__ void i8_store(const I8Args& a, int t, int n, int32_t acc, float gm, float s) {
-    const int64_t o = static_cast<int64_t>(t) * a.N + n;
-    const float v = __fmul_rn(static_cast<float>(acc), __fdiv_rn(gm, s));
+__device__ __forceinline__ void i8_store(const I8Args& a, int64_t o, int32_t acc, float gm, float r) {
+    const float v = __fmul_rn(__fmul_rn(static_cast<float>(acc), gm), r);
     if constexpr (kBf16Out) static_cast<uint16_t*>(a.y)[o] = float_to_bf16_bits(v);
     else static_cast<float*>(a.y)[o] = v;
     if (a.acc != nullptr) a.acc[o] = acc;
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4);
+            mbar_init(&tempty[b], 8);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     } else {
         // ----------------------------------------------------------------- epilogue
         const int quad = warp & 3;              // TMEM lanes [32 quad, 32 quad + 32): weight rows
+        const int half = (warp - 2) >> 2;       // 16-token chunks half, half + 2, ...
         const int r = quad * 32 + lane;
         int tcount = 0;
         for (int tile = unit0; tile < tiles; tile += units, ++tcount) {
@@ -215,18 +218,26 @@ __global__ void __launch_bounds__(kI8Threads, 1)
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                    static_cast<uint32_t>(b * a.bt);
             if (quad * 32 < a.rows) {
-                for (int c0 = 0; c0 < tend; c0 += 16) {
+                for (int c0 = half * 16; c0 < tend; c0 += 32) {
                     uint32_t v[16];
+                    float rt[16];
                     __syncwarp();
                     tmem_ld_32x32b_x16(t_row + c0, v);
+                    if (a.splits == 1) {
+                        // 1 / s_t of the chunk's tokens: a lane computes one, the warp reads all
+                        const float mine = c0 + (lane & 15) < tend ? __frcp_rn(__ldg(a.sx + t0 + c0 + (lane & 15))) : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) rt[i] = __shfl_sync(0xffffffffu, mine, i);
+                    }
                     tmem_ld_wait();
                     if (a.splits == 1) {
+                        const int64_t o = static_cast<int64_t>(t0 + c0) * a.N + n;
                         if (live) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 if (c0 + i < tend)
-                                    i8_store<kBf16Out>(a, t0 + c0 + i, n, static_cast<int32_t>(v[i]), gm,
-                                                       __ldg(a.sx + t0 + c0 + i));
+                                    i8_store<kBf16Out>(a, o + static_cast<int64_t>(i) * a.N, static_cast<int32_t>(v[i]),
+                                                       gm, rt[i]);
                         }
                     } else {
                         // this CTA's partial sums [token][row], over the ring: every load has been
@@ -263,13 +274,13 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                     if (q < a.splits) {
                         sum.x += v[q].x; sum.y += v[q].y; sum.z += v[q].z; sum.w += v[q].w;
                     }
-                const float s = __ldg(a.sx + t0 + c);
+                const float rt = __frcp_rn(__ldg(a.sx + t0 + c));
+                const int64_t o = static_cast<int64_t>(t0 + c) * a.N + n0 + lane * 4;
                 const int32_t e[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = lane * 4 + i;
-                    if (r < a.rows && n0 + r < a.N)
-                        i8_store<kBf16Out>(a, t0 + c, n0 + r, e[i], __ldg(a.gamma + n0 + r), s);
+                    if (r < a.rows && n0 + r < a.N) i8_store<kBf16Out>(a, o + i, e[i], __ldg(a.gamma + n0 + r), rt);
                 }
             }
         }

@@ -41,6 +41,8 @@ enum TcEpilogue : int {
     kEpiLinearF32 = 3,    // y = acc * (gamma / s_t) -> fp32
     kEpiLinearColBf16 = 4,  // y = acc * (gamma_n / s_t) -> bf16 (one scale per output column; 2-SM kernel only)
     kEpiLinearColF32 = 5,   // y = acc * (gamma_n / s_t) -> fp32 (2-SM kernel only)
+    kEpiInt8Bf16 = 6,       // y = (acc * gamma_n) * (1 / s_t) -> bf16 (2-SM kernel only)
+    kEpiInt8F32 = 7,        // y = (acc * gamma_n) * (1 / s_t) -> fp32 (2-SM kernel only)
 };
 
 constexpr int kTcStages = 4;
@@ -68,11 +70,16 @@ __host__ __device__ constexpr size_t tc_smem_bytes() {
            (2 * kTcStages + 4) * sizeof(uint64_t) + 16;
 }
 
-__host__ __device__ constexpr bool epi_is_col(int e) { return e == kEpiLinearColBf16 || e == kEpiLinearColF32; }
+__host__ __device__ constexpr bool epi_is_int8(int e) { return e == kEpiInt8Bf16 || e == kEpiInt8F32; }
+__host__ __device__ constexpr bool epi_is_col(int e) {
+    return e == kEpiLinearColBf16 || e == kEpiLinearColF32 || epi_is_int8(e);
+}
 __host__ __device__ constexpr bool epi_is_linear(int e) {
     return e == kEpiLinearBf16 || e == kEpiLinearF32 || epi_is_col(e);
 }
-__host__ __device__ constexpr bool epi_is_bf16(int e) { return e == kEpiLinearBf16 || e == kEpiLinearColBf16; }
+__host__ __device__ constexpr bool epi_is_bf16(int e) {
+    return e == kEpiLinearBf16 || e == kEpiLinearColBf16 || e == kEpiInt8Bf16;
+}
 // Output columns per 128-byte chunk.
 __host__ __device__ constexpr int epi_chunk_cols(int e) { return epi_is_bf16(e) ? 64 : 32; }
 
@@ -592,12 +599,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 // the factor of chunk column i: gamma / s_t, or fl(gamma_n / s_t) per column
                 // (correctly rounded from the row's reciprocal with two FMA corrections)
                 auto fac = [&](int i) -> float {
-                    if constexpr (epi_is_col(kEpi)) {
+                    if constexpr (epi_is_int8(kEpi)) {
+                        return cr;
+                    } else if constexpr (epi_is_col(kEpi)) {
                         const int c = col0 + i < args.N ? col0 + i : args.N - 1;
                         return row_ok ? div_by_scale(__ldg(args.gamma + c), cs, cr) : 0.0f;
                     } else {
                         return cs;
                     }
+                };
+                // the accumulators as fp32, times gamma_n where the epilogue multiplies by it first (the
+                // same 16 bytes for every lane; N is a multiple of 16, so a vector is in or out whole)
+                auto val = [&](int i) -> float { return static_cast<float>(static_cast<int32_t>(r(i))); };
+                float gn[epi_is_int8(kEpi) ? kChunkCols : 1];
+                if constexpr (epi_is_int8(kEpi)) {
+#pragma unroll
+                    for (int j = 0; j < kChunkCols / 4; ++j) {
+                        const int c = col0 + 4 * j < args.N ? col0 + 4 * j : 0;
+                        const float4 q = __ldg(reinterpret_cast<const float4*>(args.gamma + c));
+                        gn[4 * j] = q.x; gn[4 * j + 1] = q.y; gn[4 * j + 2] = q.z; gn[4 * j + 3] = q.w;
+                    }
+                }
+                auto scaled = [&](int i) -> float {
+                    if constexpr (epi_is_int8(kEpi)) return __fmul_rn(__fmul_rn(val(i), gn[i]), fac(i));
+                    else return __fmul_rn(val(i), fac(i));
                 };
                 uint4 v[8];
                 if constexpr (epi_is_bf16(kEpi)) {
@@ -606,8 +631,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float lo = __fmul_rn(static_cast<float>(static_cast<int32_t>(r(8 * j + 2 * e))), fac(8 * j + 2 * e));
-                            const float hi = __fmul_rn(static_cast<float>(static_cast<int32_t>(r(8 * j + 2 * e + 1))), fac(8 * j + 2 * e + 1));
+                            const float lo = scaled(8 * j + 2 * e);
+                            const float hi = scaled(8 * j + 2 * e + 1);
                             w[e] = (uint32_t)float_to_bf16_bits(lo) | ((uint32_t)float_to_bf16_bits(hi) << 16);
                         }
                         v[j] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -619,8 +644,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t raw = r(4 * j + e);
-                            if constexpr (kEpi == kEpiLinearF32 || kEpi == kEpiLinearColF32)
-                                f[e] = __fmul_rn(static_cast<float>(static_cast<int32_t>(raw)), fac(4 * j + e));
+                            if constexpr (epi_is_linear(kEpi))
+                                f[e] = scaled(4 * j + e);
                             else if constexpr (kEpi == kEpiScaleF32)
                                 f[e] = __fmul_rn(gm, __uint_as_float(raw));
                             else

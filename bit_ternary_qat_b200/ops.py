@@ -726,7 +726,7 @@ def bitlinear_quant_weight_int8(W: torch.Tensor, want_i8: bool = True, want_bf16
 def bitlinear_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tensor, gamma_rows: torch.Tensor,
                           out_dtype=torch.bfloat16, want_acc: bool = False, y: Optional[torch.Tensor] = None,
                           acc: Optional[torch.Tensor] = None):
-    """y[t,n] = acc[t,n] * (gamma_rows[n] / sx[t]) from 8-bit codes, one token to many.  Returns
+    """y[t,n] = acc[t,n] * gamma_rows[n] / sx[t] from 8-bit codes, one token to many.  Returns
     (y [T,N], acc [T,N] i32 or None)."""
     if not xq.is_cuda:
         raise ValueError("xq must be a CUDA tensor")

@@ -449,7 +449,7 @@ BL_API bl_status bitlinear_quant_weight_int8(const float* W, int64_t N, int64_t 
 
 /* The product, from one token to a whole prompt:
  *   acc[t,n] = sum_k Xq[t,k] * W_q[n,k]                          exact int32 (codes -128..127)
- *   Y[t,n]   = fl32( (float)acc[t,n] * fl32(gamma_rows[n] / sx[t]) )    rounded to y_dt
+ *   Y[t,n]   = fl32( fl32((float)acc[t,n] * gamma_rows[n]) * fl32(1 / sx[t]) )   rounded to y_dt
  * Xq int8 [T x K], sx fp32 [T] (bitlinear_act_quant's or bitlinear_residual_norm's), Wq_i8 int8
  * [N x K], gamma_rows fp32 [N], Y [T x N] of y_dt, acc int32 [T x N] optional.  K < 2^17 (the
  * int32 sums cannot wrap).  One launch. */

@@ -1,6 +1,6 @@
 """The 8-bit weight quantiser and the 8-bit linear, all compared exactly: the codes and scales
 against one fp32 rounding an operation, the accumulators as whole numbers, Y as
-fl(acc * fl(gamma_n / s_t)) rounded once to its type."""
+fl(fl(acc gamma_n) fl(1 / s_t)) rounded once to its type."""
 import numpy as np
 import pytest
 import torch
@@ -29,8 +29,8 @@ def check(bl, T, N, K, seed=0, out_dtype=F):
     assert bl.check_device_status() == 0
     want = xq.double() @ wq.double().t()              # whole numbers below 2^53
     assert torch.equal(acc.double(), want)
-    f = torch.from_numpy(gm.cpu().numpy()[None, :] / sx.cpu().numpy()[:, None])
-    yw = (acc.cpu().to(F) * f).to(out_dtype)
+    r = torch.from_numpy(np.float32(1) / sx.cpu().numpy()[:, None])
+    yw = (acc.cpu().to(F) * gm.cpu()[None, :] * r).to(out_dtype)
     assert torch.equal(y.cpu(), yw)
     assert none is None and torch.equal(y2, y)
 
