@@ -1093,18 +1093,14 @@ bl_status launch_residual_norm_bwd(const bl::RnBwdArgs& a, cudaStream_t st, cons
 // ------------------------------------------------------------------------------------
 // 8-bit linear, few tokens
 // ------------------------------------------------------------------------------------
-struct I8Plan {
-    int rows, splits, stages, a_pitch, grid;
-};
-
 // Clusters of `splits` CTAs (all the shared memory, one CTA per SM) that are resident at once.
-template <bool kBf16Out>
+template <bool kBf16Out, int kpb>
 bl_status i8_slots(int splits, int dev_id, const DeviceInfo& dev, int* out) {
     static std::atomic<int> cache[64][4] = {};
     const int idx = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
     int n = cache[dev_id][idx].load();
     if (n == 0) {
-        auto kern = bl::gemm_int8_few_kernel<kBf16Out>;
+        auto kern = bl::gemm_int8_few_kernel<kBf16Out, kpb>;
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_optin);
         if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         if (splits == 1) {
@@ -1131,61 +1127,17 @@ bl_status i8_slots(int splits, int dev_id, const DeviceInfo& dev, int* out) {
     return BL_OK;
 }
 
-template <bool kBf16Out>
-bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq,
-                              const float* gamma_rows, int64_t N, void* Y, int32_t* acc, cudaStream_t st,
-                              const DeviceInfo& dev) {
-    int dev_id = 0;
-    cudaGetDevice(&dev_id);
-    if (dev_id < 0 || dev_id >= 64) return fail(BL_ERR_DEVICE, "device ordinal %d out of range", dev_id);
-    bl::I8Args a{};
-    a.T = (int)T; a.N = (int)N; a.K = (int)K;
-    a.bt = (int)std::min<int64_t>((T + 15) / 16 * 16, bl::kI8MaxTokens);
-    a.t_tiles = (int)((T + a.bt - 1) / a.bt);
-    a.k_blocks = (int)((K + 127) / 128);
-    // Rows per tile and K split with the fewest bytes through the busiest SM (weight rows and
-    // tokens, 128 bytes of each per k-block); a split pays for its join (two cluster barriers and
-    // the partial sums' way through distributed shared memory), counted as kJoin more row-blocks
-    // and the sums' own bytes.
-    constexpr int64_t kJoin = 600;
-    int64_t best = -1;
-    for (int sp = 1; sp <= 8; sp *= 2) {
-        if (sp > 1 && a.k_blocks < 4 * sp) break;
-        int slots = 0;
-        BL_TRY((i8_slots<kBf16Out>(sp, dev_id, dev, &slots)));
-        for (int64_t w = 1;; ++w) {
-            const int64_t n_tiles = std::max<int64_t>(1, slots * w / a.t_tiles);
-            int64_t rows = (N + n_tiles - 1) / n_tiles;
-            if (sp > 1) rows = (rows + 3) / 4 * 4;
-            if (rows > 128) continue;
-            const int64_t kbs = (a.k_blocks + sp - 1) / sp;
-            const int64_t cost = w * (kbs * (rows + a.bt) + (sp > 1 ? kJoin + 4 * a.bt : 0));
-            if (best < 0 || cost < best) {
-                best = cost;
-                a.rows = (int)rows;
-                a.splits = sp;
-            }
-            break;
-        }
-    }
-    a.n_tiles = (int)((N + a.rows - 1) / a.rows);
-    a.a_pitch = (a.rows + 7) / 8 * 1024;
-    a.stages = bl::kI8MaxStages;
-    while (a.stages > 2 && bl::i8_smem_bytes(a.stages, a.a_pitch, a.bt) > (size_t)dev.max_smem_optin) --a.stages;
-    const size_t smem = bl::i8_smem_bytes(a.stages, a.a_pitch, a.bt);
+template <bool kBf16Out, int kpb>
+bl_status launch_int8_few(const CUtensorMap& tw, const CUtensorMap& tx, const bl::I8Args& a, int64_t tiles,
+                          cudaStream_t st, int dev_id, const DeviceInfo& dev) {
+    auto kern = bl::gemm_int8_few_kernel<kBf16Out, kpb>;
+    int slots = 0;
+    BL_TRY((i8_slots<kBf16Out, kpb>(a.splits, dev_id, dev, &slots)));   // sets the kernel's attributes
+    const size_t smem = bl::i8_smem_bytes(a.stages, kpb, a.a_pitch, a.bt);
     // a split's partial sums lie over the ring
-    BL_REQUIRE(smem <= (size_t)dev.max_smem_optin &&
-                   (a.splits == 1 || bl::i8_ring_bytes(a.stages, a.a_pitch, a.bt) >= (size_t)a.bt * 512),
+    BL_REQUIRE(smem <= (size_t)dev.max_smem_optin && a.k_steps >= a.splits &&
+                   (a.splits == 1 || bl::i8_ring_bytes(a.stages, kpb, a.a_pitch, a.bt) >= (size_t)a.bt * 512),
                BL_ERR_DEVICE, "int8 GEMM: shared memory too small");
-    const int64_t per_cta = a.splits > 1 ? 1 : ((int64_t)a.n_tiles * a.t_tiles + dev.sms - 1) / dev.sms;
-    a.bufs = per_cta > 1 ? 2 : 1;
-    a.sx = sx; a.gamma = gamma_rows; a.y = Y; a.acc = acc;
-    a.wait_ns = g_wait_ns.load();
-    CUtensorMap tw, tx;
-    BL_TRY(make_tmap(&tw, Wq, kTmU8, (uint64_t)K, (uint64_t)N, 128, (uint32_t)a.rows));
-    BL_TRY(make_tmap(&tx, Xq, kTmU8, (uint64_t)K, (uint64_t)T, 128, (uint32_t)a.bt));
-    const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
-    auto kern = bl::gemm_int8_few_kernel<kBf16Out>;
     if (a.splits == 1) {
         pdl_launch(kern, dim3((unsigned)std::min<int64_t>(tiles, dev.sms)), dim3(bl::kI8Threads), smem, st, tw, tx, a);
     } else {
@@ -1205,6 +1157,63 @@ bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int6
         cudaLaunchKernelEx(&cfg, kern, tw, tx, a);
     }
     return launched("gemm_int8_few");
+}
+
+template <bool kBf16Out>
+bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq,
+                              const float* gamma_rows, int64_t N, void* Y, int32_t* acc, cudaStream_t st,
+                              const DeviceInfo& dev) {
+    int dev_id = 0;
+    cudaGetDevice(&dev_id);
+    if (dev_id < 0 || dev_id >= 64) return fail(BL_ERR_DEVICE, "device ordinal %d out of range", dev_id);
+    bl::I8Args a{};
+    a.T = (int)T; a.N = (int)N; a.K = (int)K;
+    a.bt = (int)std::min<int64_t>((T + 15) / 16 * 16, bl::kI8MaxTokens);
+    a.t_tiles = (int)((T + a.bt - 1) / a.bt);
+    const int k_blocks = (int)((K + 127) / 128);
+    // Rows per tile and K split with the least time on the busiest SM, in rows of 128 bytes: of each
+    // k-block the weight rows and the tokens, and kStep for issuing it (0.08 us); a split pays for
+    // its join (two cluster barriers and the way through distributed shared memory, 1 us) and for
+    // the partial sums' own bytes.  One token: 4096 x 4096 7.2 us split in 4 (116 rows), 7.6 whole
+    // (28 rows); 11008 x 4096 20.0 split in 4, 10.7 whole (75 rows).
+    constexpr int64_t kStep = 28, kJoin = 350;
+    int64_t best = -1;
+    for (int sp = 1; sp <= 8; sp *= 2) {
+        if (sp > 1 && k_blocks < 4 * sp) break;
+        int slots = 0;
+        BL_TRY((i8_slots<kBf16Out, 1>(sp, dev_id, dev, &slots)));
+        for (int64_t w = 1;; ++w) {
+            const int64_t n_tiles = std::max<int64_t>(1, slots * w / a.t_tiles);
+            int64_t rows = (N + n_tiles - 1) / n_tiles;
+            if (sp > 1) rows = (rows + 3) / 4 * 4;
+            if (rows > 128) continue;
+            const int64_t kbs = (k_blocks + sp - 1) / sp;
+            const int64_t cost = w * (kbs * (rows + a.bt + kStep) + (sp > 1 ? kJoin + 4 * a.bt : 0));
+            if (best < 0 || cost < best) {
+                best = cost;
+                a.rows = (int)rows;
+                a.splits = sp;
+            }
+            break;
+        }
+    }
+    a.n_tiles = (int)((N + a.rows - 1) / a.rows);
+    a.a_pitch = (a.rows + 7) / 8 * 1024;
+    const size_t limit = (size_t)dev.max_smem_optin;
+    const int kpb = bl::i8_smem_bytes(4, 2, a.a_pitch, a.bt) <= limit ? 2 : 1;
+    a.k_steps = (k_blocks + kpb - 1) / kpb;
+    a.stages = std::min(bl::kI8MaxStages, std::max(2, a.k_steps));
+    while (a.stages > 2 && bl::i8_smem_bytes(a.stages, kpb, a.a_pitch, a.bt) > limit) --a.stages;
+    const int64_t per_cta = a.splits > 1 ? 1 : ((int64_t)a.n_tiles * a.t_tiles + dev.sms - 1) / dev.sms;
+    a.bufs = per_cta > 1 ? 2 : 1;
+    a.sx = sx; a.gamma = gamma_rows; a.y = Y; a.acc = acc;
+    a.wait_ns = g_wait_ns.load();
+    CUtensorMap tw, tx;
+    BL_TRY(make_tmap(&tw, Wq, kTmU8, (uint64_t)K, (uint64_t)N, 128, (uint32_t)a.rows));
+    BL_TRY(make_tmap(&tx, Xq, kTmU8, (uint64_t)K, (uint64_t)T, 128, (uint32_t)a.bt));
+    const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
+    if (kpb == 2) return launch_int8_few<kBf16Out, 2>(tw, tx, a, tiles, st, dev_id, dev);
+    return launch_int8_few<kBf16Out, 1>(tw, tx, a, tiles, st, dev_id, dev);
 }
 
 // |Xq|, |Wq| <= 128: a sum of K products stays below 2^31 for K < 2^17.

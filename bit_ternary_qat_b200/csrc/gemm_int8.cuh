@@ -32,10 +32,10 @@ struct I8Args {
     int rows;          // R: weight rows per tile
     int bt;            // token tile (multiple of 16)
     int n_tiles, t_tiles;
-    int k_blocks;
+    int k_steps;       // stages' worth of K
     int stages;
     int bufs;          // tiles whose accumulators fit TMEM at once: 1 or 2
-    int a_pitch;       // bytes of a stage's weight slot (multiple of 1024)
+    int a_pitch;       // bytes of a k-block's weight slot (multiple of 1024)
     int splits;        // cluster size along K
     const float* sx;
     const float* gamma;
@@ -46,13 +46,13 @@ struct I8Args {
 
 // Shared memory behind the 1024-byte aligned start: weight slots, token slots, barriers.  The
 // MMA reads 128 rows from each weight slot's start, so 16 KB must be readable behind the last.
-__host__ __device__ inline size_t i8_ring_bytes(int stages, int a_pitch, int bt) {
-    const size_t a = (size_t)stages * a_pitch, b = (size_t)stages * bt * 128;
-    const size_t need = (size_t)(stages - 1) * a_pitch + 16384;
+__host__ __device__ inline size_t i8_ring_bytes(int stages, int kpb, int a_pitch, int bt) {
+    const size_t a = (size_t)stages * kpb * a_pitch, b = (size_t)stages * kpb * bt * 128;
+    const size_t need = (size_t)(stages * kpb - 1) * a_pitch + 16384;
     return a + b < need ? need : a + b;
 }
-__host__ __device__ inline size_t i8_smem_bytes(int stages, int a_pitch, int bt) {
-    return 1024 + i8_ring_bytes(stages, a_pitch, bt) + (2 * kI8MaxStages + 4) * sizeof(uint64_t) + 16;
+__host__ __device__ inline size_t i8_smem_bytes(int stages, int kpb, int a_pitch, int bt) {
+    return 1024 + i8_ring_bytes(stages, kpb, a_pitch, bt) + (2 * kI8MaxStages + 4) * sizeof(uint64_t) + 16;
 }
 
 // 16 consecutive columns of 32 TMEM lanes.
@@ -82,15 +82,21 @@ __device__ __forceinline__ void i8_store(const I8Args& a, int64_t o, int32_t acc
     if (a.acc != nullptr) a.acc[o] = acc;
 }
 
-template <bool kBf16Out>
+// kpb: k-blocks of 128 bytes in a stage.  A stage costs its waits, its expect and its commit (about
+// 300 cycles, whatever it carries), so it carries as many as leave four stages; fixed at compile time,
+// since the two issuing threads' own instructions are what counts (2048 x 16384, one token, without a
+// K split: 24.7 us with 1, 17.5 with 2; 23.3 with 2 when the loops take it from the arguments).
+template <bool kBf16Out, int kpb>
 __global__ void __launch_bounds__(kI8Threads, 1)
     gemm_int8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                          const I8Args a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_align1024(smem_raw);
     uint8_t* sA = smem;
-    uint8_t* sB = smem + static_cast<size_t>(a.stages) * a.a_pitch;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + i8_ring_bytes(a.stages, a.a_pitch, a.bt));
+    uint8_t* sB = smem + static_cast<size_t>(a.stages) * kpb * a.a_pitch;
+    const uint32_t a_stage = static_cast<uint32_t>(kpb * a.a_pitch), b_kb = static_cast<uint32_t>(a.bt) * 128u,
+                   b_stage = kpb * b_kb;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + i8_ring_bytes(a.stages, kpb, a.a_pitch, a.bt));
     uint64_t* empty = full + kI8MaxStages;
     uint64_t* tfull = empty + kI8MaxStages;
     uint64_t* tempty = tfull + 2;
@@ -130,9 +136,9 @@ __global__ void __launch_bounds__(kI8Threads, 1)
     const int rank = a.splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int unit0 = blockIdx.x / a.splits, units = gridDim.x / a.splits;
     const int tiles = a.n_tiles * a.t_tiles;
-    const int kb0 = static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / a.splits);
-    const int kb1 = static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / a.splits);
-    const uint32_t stage_tx = static_cast<uint32_t>(a.rows + a.bt) * 128u;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(a.k_steps) * rank / a.splits);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(a.k_steps) * (rank + 1) / a.splits);
+    const uint32_t stage_tx = static_cast<uint32_t>(a.rows + a.bt) * (128u * kpb);
 
     if (warp == 0) {
         // ----------------------------------------------------------------- producer
@@ -146,8 +152,11 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&empty[s], ph ^ 1u, lim, abort_flag)) { ok = false; break; }
                     mbar_arrive_expect_tx(&full[s], stage_tx);
-                    tma_load_2d(sA + static_cast<size_t>(s) * a.a_pitch, &tmW, &full[s], kb * 128, n0);
-                    tma_load_2d(sB + static_cast<size_t>(s) * a.bt * 128, &tmX, &full[s], kb * 128, t0);
+#pragma unroll
+                    for (int q = 0; q < kpb; ++q) {   // past the end of K the boxes are filled with zeros
+                        tma_load_2d(sA + s * a_stage + q * a.a_pitch, &tmW, &full[s], (kb * kpb + q) * 128, n0);
+                        tma_load_2d(sB + s * b_stage + q * b_kb, &tmX, &full[s], (kb * kpb + q) * 128, t0);
+                    }
                     ++posted;
                     if (++s == a.stages) { s = 0; ph ^= 1u; }
                 }
@@ -178,13 +187,16 @@ __global__ void __launch_bounds__(kI8Threads, 1)
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&full[s], ph, lim, abort_flag)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a_base = smem_u32(sA + static_cast<size_t>(s) * a.a_pitch);
-                    const uint32_t b_base = smem_u32(sB + static_cast<size_t>(s) * a.bt * 128);
+                    const uint32_t a_base = smem_u32(sA) + s * a_stage, b_base = smem_u32(sB) + s * b_stage;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma<true>(d_tmem, umma_desc_sw128(a_base + kk * 32, 16, 1024),
-                                     umma_desc_sw128(b_base + kk * 32, 16, 1024), idesc,
-                                     (kb != kb0 || kk != 0) ? 1u : 0u);
+                    for (int q = 0; q < kpb; ++q) {
+                        const uint64_t ad = umma_desc_sw128(a_base + q * a.a_pitch, 16, 1024),
+                                       bd = umma_desc_sw128(b_base + q * b_kb, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)      // 32 bytes of K: 2 in the descriptors' address fields
+                            tc_mma<true>(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc,
+                                         (kb != kb0 || q != 0 || kk != 0) ? 1u : 0u);
+                    }
                     tc_commit(&empty[s]);
                     if (++s == a.stages) { s = 0; ph ^= 1u; }
                 }
