@@ -14,6 +14,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 MAIN = os.path.join(SRC_DIR, "bitlinear.cu")
 HEADER = os.path.join(ROOT, "include", "bitlinear.h")
 LIB = os.path.join(HERE, "libbitlinear.so")
+MARSHAL_SRC = os.path.join(SRC_DIR, "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")      # tensor-level calls in C++, over libbitlinear.so's C ABI
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -45,7 +47,32 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """The C++ part of the binding (g++, against the installed torch)."""
+    if not force and os.path.exists(MARSHAL) and all(
+            os.path.getmtime(s) <= os.path.getmtime(MARSHAL) for s in (MARSHAL_SRC, HEADER)):
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = MARSHAL + ".tmp.%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *[a for d in cpp_extension.include_paths() for a in ("-isystem", d)],
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
+           "-isystem", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp,
+           "-L", lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_marshal(force, verbose)
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()

@@ -1,13 +1,14 @@
 """Tensor-level binding of the C ABI: same names as the C entry points.
 
-Argument marshalling only: check that tensors are contiguous CUDA tensors of the
+Argument marshalling only (for the calls whose kernels take microseconds in C++, see
+csrc/marshal.cpp): check that tensors are contiguous CUDA tensors of the
 expected dtype, allocate outputs that the caller did not pass (torch is used for
 device memory and streams), pass ``data_ptr()`` values and the current CUDA stream
 to libbitlinear.so.  Every step of the computation runs in the library's kernels.
 """
 from __future__ import annotations
 
-from array import array
+import ctypes
 from typing import Optional
 
 import torch
@@ -47,6 +48,27 @@ def _same(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
         return t.data_ptr()
     raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
                      f"{tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+# The C++ part of this binding: the calls whose kernels run for a few microseconds.
+_marshal_module = None
+_MARSHALLED = ("bitlinear_workspace_bytes", "bitlinear_residual_norm", "bitlinear_residual_norm_backward",
+               "bitlinear_grad_norm", "bitlinear_clip_grads", "bitlinear_quant_weight_int8", "bitlinear_linear_int8")
+
+
+def _raise(name: str, status: int):
+    raise _lib.BitLinearError(name, status, _lib.last_error())
+
+
+def _marshal():
+    """Load (once) the C++ part and give it the library's entry points; raises if either is missing."""
+    global _marshal_module
+    if _marshal_module is None:
+        L = _lib.lib()
+        from . import _marshal as module
+        module.init(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _MARSHALLED), _raise)
+        _marshal_module = module
+    return _marshal_module
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream().cuda_stream without the Stream object
@@ -477,113 +499,23 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
 # global gradient norm and clipping
 # ----------------------------------------------------------------------------------
 
-# unbound, to be mapped over lists of many tensors
-_T = torch.Tensor
-_t_numel, _t_ptr, _t_device, _t_dense, _t_dtype = (_T.numel, _T.data_ptr, _T.get_device, _T.is_contiguous,
-                                                   _T.dtype.__get__)
-
-
-def _grad_lists(grads, out):
-    """Device, and host arrays of addresses, output addresses (or None), sizes and types."""
-    if len(grads) == 0:
-        raise ValueError("grads must not be empty")
-    numel, types = list(map(_t_numel, grads)), list(map(_t_dtype, grads))
-    every = grads
-    if out is not None:
-        if list(map(_t_numel, out)) != numel or list(map(_t_dtype, out)) != types:
-            raise ValueError("out must have the sizes and types of grads")
-        every = [*grads, *out]
-    where = set(map(_t_device, every))
-    if len(where) != 1 or -1 in where or not all(map(_t_dense, every)):
-        raise ValueError("gradients and outputs must be contiguous CUDA tensors on one device")
-    try:
-        codes = array("i", map(_DT.__getitem__, types))
-    except KeyError as e:
-        raise ValueError(f"unsupported dtype {e.args[0]}") from None
-    return (grads[0].device, array("q", map(_t_ptr, grads)), None if out is None else array("q", map(_t_ptr, out)),
-            array("q", numel), codes)
-
-
-def _at(a: array) -> int:
-    return a.buffer_info()[0]
-
-
-# the clip's workspace is the same for every list
-_CLIP_WS = None
-
-
-def _norm_outputs(dev, norm, coef, ws):
-    global _CLIP_WS
-    if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
-    else:
-        _same(norm, "norm", torch.float32, (1,), dev)
-    if coef is None:
-        coef = torch.empty_like(norm)
-    else:
-        _same(coef, "coef", torch.float32, (1,), dev)
-    if ws is None:
-        if _CLIP_WS is None:
-            _CLIP_WS = workspace_bytes(1, 1, 1)
-        ws = torch.empty(_CLIP_WS, dtype=torch.uint8, device=dev)
-    return norm, coef, ws
-
-
 def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tensor] = None,
                         coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """Global L2 norm of a list of gradients (fp32 or bf16, any shapes) and its clip coefficient.
     Returns dict(norm [1] f32, coef [1] f32); coef goes into bitlinear_optimizer_step."""
-    dev, ptrs, _, numel, types = _grad_lists(grads, None)
-    norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    _call(dev, "bitlinear_grad_norm", _at(ptrs), _at(numel), _at(types), len(ptrs), max_norm, norm.data_ptr(), coef.data_ptr(),
-          ws.data_ptr(), ws.numel() * ws.element_size())
-    return {"norm": norm, "coef": coef}
+    return _marshal().grads(False, grads, max_norm, None, norm, coef, ws)
 
 
 def bitlinear_clip_grads(grads, max_norm: float = 1.0, out=None, norm: Optional[torch.Tensor] = None,
                          coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """Scales a list of gradients by the clip coefficient of their global norm, in place or into
     ``out``.  Returns dict(norm [1] f32, coef [1] f32, grads: the scaled list)."""
-    dev, ptrs, outs, numel, types = _grad_lists(grads, out)
-    if outs is None:
-        outs = ptrs
-    n = len(ptrs)
-    if len(set(outs)) != n and len({p for p, k in zip(outs, numel) if k}) != sum(1 for k in numel if k):
-        raise ValueError("a gradient is written twice")
-    norm, coef, ws = _norm_outputs(dev, norm, coef, ws)
-    _call(dev, "bitlinear_clip_grads", _at(ptrs), _at(outs), _at(numel), _at(types), n, max_norm, norm.data_ptr(),
-          coef.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
-    return {"norm": norm, "coef": coef, "grads": grads if out is None else out}
+    return _marshal().grads(True, grads, max_norm, out, norm, coef, ws)
 
 
 # ----------------------------------------------------------------------------------
 # residual norms: between two BitLinears
 # ----------------------------------------------------------------------------------
-
-GATE_NONE, GATE_SCALAR, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = range(5)
-
-
-def _gate(gate: Optional[torch.Tensor], T: int, K: int, y_dtype, dev):
-    """(gate kind, address): [1] scalar, [K] channel, [T, 1] token (fp32), [T, K] element (y's type)."""
-    if gate is None:
-        return GATE_NONE, None
-    if gate.dim() == 2 and gate.shape[1] == 1 and (K != 1 or gate.dtype is torch.float32):
-        return GATE_TOKEN, _same(gate, "gate", torch.float32, (T, 1), dev)
-    if gate.dim() == 2:
-        return GATE_ELEMENT, _same(gate, "gate", y_dtype, (T, K), dev)
-    if gate.dim() == 1 and gate.shape[0] == 1:
-        return GATE_SCALAR, _same(gate, "gate", torch.float32, (1,), dev)
-    return GATE_CHANNEL, _same(gate, "gate", torch.float32, (K,), dev)
-
-
-def _residual_types(x: torch.Tensor, y: torch.Tensor):
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a CUDA tensor [T, K]")
-    if (x.dtype, y.dtype) not in ((torch.float32, torch.float32), (torch.bfloat16, torch.bfloat16),
-                                  (torch.float32, torch.bfloat16)):
-        raise ValueError(f"unsupported types: residual {x.dtype}, block {y.dtype}")
-    return x.shape, x.device
-
 
 def bitlinear_residual_norm(x: torch.Tensor, y: torch.Tensor, post_norm: bool = True,
                             g_post: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
@@ -596,51 +528,8 @@ def bitlinear_residual_norm(x: torch.Tensor, y: torch.Tensor, post_norm: bool = 
     Returns dict(x [T,K] of x's type, r_post [T] f32 with post_norm, and by mode: r_pre [T] f32,
     xq [T,K] i8, sx [T] f32, xdq [T,K] of y's type; or r_pre, h [T,K] of y's type).
     out["x"] may be x itself."""
-    shape, dev = _residual_types(x, y)
-    T, K = shape
-    xt, yt, f32, row = x.dtype, y.dtype, torch.float32, (T,)
-    px, py = _same(x, "x", xt, shape, dev), _same(y, "y", yt, shape, dev)
-    kind, pgate = (GATE_NONE, None) if gate is None else _gate(gate, T, K, yt, dev)
-    p_post = None if g_post is None else _same(g_post, "g_post", f32, (K,), dev)
-    p_pre = None if g_pre is None else _same(g_pre, "g_pre", f32, (K,), dev)
-    if mode not in ("quant", "norm", "none"):
-        raise ValueError(f"mode must be 'quant', 'norm' or 'none', got {mode!r}")
-    o = {} if out is None else dict(out)
-    if out is not None:
-        for name, dtype in (("x", xt), ("h", yt), ("xq", torch.int8), ("xdq", yt)):
-            if name in o:
-                _same(o[name], name, dtype, shape, dev)
-        for name in ("r_post", "r_pre", "sx"):
-            if name in o:
-                _same(o[name], name, f32, row, dev)
-    r_post = r_pre = h = xq = sx = xdq = None
-    if "x" not in o:
-        o["x"] = torch.empty_like(x)
-    if post_norm:
-        if "r_post" not in o:
-            o["r_post"] = x.new_empty(row, dtype=f32)
-        r_post = o["r_post"].data_ptr()
-    if mode != "none":
-        if "r_pre" not in o:
-            o["r_pre"] = torch.empty_like(o["r_post"]) if post_norm else x.new_empty(row, dtype=f32)
-        r_pre = o["r_pre"].data_ptr()
-    if mode == "norm":
-        if "h" not in o:
-            o["h"] = torch.empty_like(y)
-        h = o["h"].data_ptr()
-    elif mode == "quant":
-        if "xq" not in o:
-            o["xq"] = x.new_empty(shape, dtype=torch.int8)
-        if "sx" not in o:
-            o["sx"] = torch.empty_like(o["r_pre"])
-        xq, sx = o["xq"].data_ptr(), o["sx"].data_ptr()
-        if want_xdq:
-            if "xdq" not in o:
-                o["xdq"] = torch.empty_like(y)
-            xdq = o["xdq"].data_ptr()
-    _call(dev, "bitlinear_residual_norm", px, _DT[xt], py, _DT[yt], T, K, 1 if post_norm else 0, p_post, eps_post, kind,
-          pgate, alpha, beta, p_pre, eps_pre, o["x"].data_ptr(), r_post, r_pre, h, xq, sx, xdq)
-    return o
+    return _marshal().residual_norm(x, y, post_norm, g_post, gate, alpha, beta, mode, g_pre, eps_post, eps_pre, want_xdq,
+                                    out)
 
 
 def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[torch.Tensor], x: torch.Tensor,
@@ -655,50 +544,8 @@ def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[to
     r_pre: its saved statistics.  Returns dict(dx [T,K] f32, dy [T,K] of y's type, and with
     want_dgains / want_dgate: dpost_gain [K], dpre_gain [K] f32 (with the norm in question),
     dgate as the gate).  out["dx"] may be dx or dh."""
-    shape, dev = _residual_types(x, y)
-    T, K = shape
-    xt, yt, f32, col = x.dtype, y.dtype, torch.float32, (K,)
-
-    def opt(t, name, sh):
-        return None if t is None else _same(t, name, f32, sh, dev)
-
-    px, py = _same(x, "x", xt, shape, dev), _same(y, "y", yt, shape, dev)
-    p_dx, p_dh = opt(dx, "dx", shape), opt(dh, "dh", shape)
-    p_post, p_pre = opt(r_post, "r_post", (T,)), opt(r_pre, "r_pre", (T,))
-    if dh is not None and r_pre is None:
-        raise ValueError("dh needs r_pre")
-    kind, pgate = (GATE_NONE, None) if gate is None else _gate(gate, T, K, yt, dev)
-    want_post, want_pre = want_dgains and r_post is not None, want_dgains and dh is not None
-    want_dgate = want_dgate and gate is not None
-    o = {} if out is None else dict(out)
-    if out is not None:
-        for name, sh, dtype in (("dx", shape, f32), ("dy", shape, yt), ("dpost_gain", col, f32),
-                                ("dpre_gain", col, f32)) + ((("dgate", gate.shape, gate.dtype),) if want_dgate else ()):
-            if name in o:
-                _same(o[name], name, dtype, sh, dev)
-    if "dx" not in o:
-        o["dx"] = torch.empty_like(dh if dx is None else dx) if dx is not None or dh is not None else x.new_empty(
-            shape, dtype=f32)
-    if "dy" not in o:
-        o["dy"] = torch.empty_like(y)
-    if want_post and "dpost_gain" not in o:
-        o["dpost_gain"] = x.new_empty(col, dtype=f32)
-    if want_pre and "dpre_gain" not in o:
-        o["dpre_gain"] = x.new_empty(col, dtype=f32)
-    if want_dgate and "dgate" not in o:
-        o["dgate"] = torch.empty_like(gate)
-    ws_bytes = 0
-    if ws is None:
-        if want_post or want_pre or (want_dgate and kind in (GATE_SCALAR, GATE_CHANNEL)):
-            ws = workspace(T, 16, K, dev)
-    if ws is not None:
-        ws_bytes = ws.numel() * ws.element_size()
-    _call(dev, "bitlinear_residual_norm_backward", p_dx, p_dh, px, _DT[xt], py, _DT[yt], T, K,
-          0 if r_post is None else 1, opt(g_post, "g_post", col), p_post, kind, pgate, alpha, beta,
-          opt(g_pre, "g_pre", col), p_pre, o["dx"].data_ptr(), o["dy"].data_ptr(),
-          o["dpost_gain"].data_ptr() if want_post else None, o["dpre_gain"].data_ptr() if want_pre else None,
-          o["dgate"].data_ptr() if want_dgate else None, _ptr(ws), ws_bytes)
-    return o
+    return _marshal().residual_norm_backward(dx, dh, x, y, r_post, r_pre, g_post, gate, alpha, beta, g_pre, want_dgains,
+                                             want_dgate, ws, out)
 
 
 # ----------------------------------------------------------------------------------
@@ -708,19 +555,7 @@ def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[to
 def bitlinear_quant_weight_int8(W: torch.Tensor, want_i8: bool = True, want_bf16: bool = True, out=None):
     """8-bit codes of the rows of W [N,K] f32.  Returns dict(gamma_rows [N] f32, wq_i8 [N,K] i8,
     wq_bf16 [N,K] bf16 (= W_q * bf16(gamma_n), the backward's operand with a gamma of 1))."""
-    _cuda(W, "W", torch.float32)
-    N, K = W.shape
-    dev = W.device
-    o = {} if out is None else dict(out)
-    for name, shape, dtype, want in (("gamma_rows", (N,), torch.float32, True), ("wq_i8", (N, K), torch.int8, want_i8),
-                                     ("wq_bf16", (N, K), torch.bfloat16, want_bf16)):
-        if name in o:
-            _same(o[name], name, dtype, shape, dev)
-        elif want:
-            o[name] = W.new_empty(shape, dtype=dtype)
-    _call(dev, "bitlinear_quant_weight_int8", W.data_ptr(), N, K, _ptr(o.get("wq_i8")), _ptr(o.get("wq_bf16")),
-          o["gamma_rows"].data_ptr())
-    return o
+    return _marshal().quant_weight_int8(W, want_i8, want_bf16, out)
 
 
 def bitlinear_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tensor, gamma_rows: torch.Tensor,
@@ -728,26 +563,7 @@ def bitlinear_linear_int8(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tenso
                           acc: Optional[torch.Tensor] = None):
     """y[t,n] = acc[t,n] * gamma_rows[n] / sx[t] from 8-bit codes, one token to many.  Returns
     (y [T,N], acc [T,N] i32 or None)."""
-    if not xq.is_cuda:
-        raise ValueError("xq must be a CUDA tensor")
-    dev = xq.device
-    T, K = xq.shape
-    N = wq_i8.shape[0]
-    px, pw = _same(xq, "xq", torch.int8, (T, K), dev), _same(wq_i8, "wq_i8", torch.int8, (N, K), dev)
-    ps, pg = _same(sx, "sx", torch.float32, (T,), dev), _same(gamma_rows, "gamma_rows", torch.float32, (N,), dev)
-    if y is None:
-        y = xq.new_empty((T, N), dtype=out_dtype)
-        py = y.data_ptr()
-    else:
-        py = _same(y, "y", y.dtype, (T, N), dev)
-    pa = None
-    if acc is not None:
-        pa = _same(acc, "acc", torch.int32, (T, N), dev)
-    elif want_acc:
-        acc = xq.new_empty((T, N), dtype=torch.int32)
-        pa = acc.data_ptr()
-    _call(dev, "bitlinear_linear_int8", px, ps, T, K, pw, pg, N, py, _dt(y), pa)
-    return y, acc
+    return _marshal().linear_int8(xq, sx, wq_i8, gamma_rows, out_dtype, want_acc, y, acc)
 
 
 def check_device_status(device=None) -> int:
