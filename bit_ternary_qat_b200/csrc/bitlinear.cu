@@ -1159,24 +1159,17 @@ bl_status launch_int8_few(const CUtensorMap& tw, const CUtensorMap& tx, const bl
     return launched("gemm_int8_few");
 }
 
+// Tiles and K split of the few-token kernel, and their cost: the least time on the busiest SM, in rows
+// of 128 bytes: of each k-block the weight rows and the tokens, and kStep for issuing it (0.08 us); a
+// split pays for its join (two cluster barriers and the way through distributed shared memory, 1 us)
+// and for the partial sums' own bytes.  One token: 4096 x 4096 7.2 us split in 4 (116 rows), 7.6 whole
+// (28 rows); 11008 x 4096 20.0 split in 4, 10.7 whole (75 rows).
 template <bool kBf16Out>
-bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq,
-                              const float* gamma_rows, int64_t N, void* Y, int32_t* acc, cudaStream_t st,
-                              const DeviceInfo& dev) {
-    int dev_id = 0;
-    cudaGetDevice(&dev_id);
-    if (dev_id < 0 || dev_id >= 64) return fail(BL_ERR_DEVICE, "device ordinal %d out of range", dev_id);
-    bl::I8Args a{};
-    a.T = (int)T; a.N = (int)N; a.K = (int)K;
-    a.bt = (int)std::min<int64_t>((T + 15) / 16 * 16, bl::kI8MaxTokens);
-    a.t_tiles = (int)((T + a.bt - 1) / a.bt);
-    const int k_blocks = (int)((K + 127) / 128);
-    // Rows per tile and K split with the least time on the busiest SM, in rows of 128 bytes: of each
-    // k-block the weight rows and the tokens, and kStep for issuing it (0.08 us); a split pays for
-    // its join (two cluster barriers and the way through distributed shared memory, 1 us) and for
-    // the partial sums' own bytes.  One token: 4096 x 4096 7.2 us split in 4 (116 rows), 7.6 whole
-    // (28 rows); 11008 x 4096 20.0 split in 4, 10.7 whole (75 rows).
+bl_status i8_plan(bl::I8Args& a, int64_t* cost_out, int dev_id, const DeviceInfo& dev) {
     constexpr int64_t kStep = 28, kJoin = 350;
+    const int k_blocks = (a.K + 127) / 128;
+    a.bt = std::min((a.T + 15) / 16 * 16, bl::kI8MaxTokens);
+    a.t_tiles = (a.T + a.bt - 1) / a.bt;
     int64_t best = -1;
     for (int sp = 1; sp <= 8; sp *= 2) {
         if (sp > 1 && k_blocks < 4 * sp) break;
@@ -1184,7 +1177,7 @@ bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int6
         BL_TRY((i8_slots<kBf16Out, 1>(sp, dev_id, dev, &slots)));
         for (int64_t w = 1;; ++w) {
             const int64_t n_tiles = std::max<int64_t>(1, slots * w / a.t_tiles);
-            int64_t rows = (N + n_tiles - 1) / n_tiles;
+            int64_t rows = (a.N + n_tiles - 1) / n_tiles;
             if (sp > 1) rows = (rows + 3) / 4 * 4;
             if (rows > 128) continue;
             const int64_t kbs = (k_blocks + sp - 1) / sp;
@@ -1197,6 +1190,37 @@ bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int6
             break;
         }
     }
+    *cost_out = best;
+    return BL_OK;
+}
+
+// Whether the few-token kernel takes T tokens: always up to 192; beyond that while the large tiles
+// (256 tokens x 256 weight rows on a pair of SMs) fill less than half the pairs and its estimate is
+// lower (us; 256 tokens: 4096 x 4096 15.3 against 21.6, 11008 x 4096 21.3 against 18.8).
+bool i8_few(const bl::I8Args& a, int64_t cost, const DeviceInfo& dev) {
+    if (a.T <= 192) return true;
+    const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256);
+    if (tiles * 4 >= dev.sms) return false;
+    const double few = 4.0 + 0.0022 * (double)cost;
+    const double large = 8.0 + 0.3 * ((a.K + 127) / 128) + 0.5 * (double)a.N * a.K / 6.5e6;
+    return few < large;
+}
+
+template <bool kBf16Out>
+bl_status run_linear_int8(const int8_t* Xq, const float* sx, int64_t T, int64_t K, const int8_t* Wq,
+                          const float* gamma_rows, int64_t N, void* Y, int32_t* acc, cudaStream_t st,
+                          const DeviceInfo& dev) {
+    int dev_id = 0;
+    cudaGetDevice(&dev_id);
+    if (dev_id < 0 || dev_id >= 64) return fail(BL_ERR_DEVICE, "device ordinal %d out of range", dev_id);
+    bl::I8Args a{};
+    a.T = (int)T; a.N = (int)N; a.K = (int)K;
+    int64_t cost = 0;
+    // from 74 pairs of 256 tokens on the large tiles fill the device by the tokens alone
+    if (T <= 74 * 256) BL_TRY(i8_plan<kBf16Out>(a, &cost, dev_id, dev));
+    if (T > 74 * 256 || !i8_few(a, cost, dev))
+        return run_linear_rows<true>(Xq, sx, T, K, Wq, gamma_rows, N, Y, kBf16Out ? BL_BF16 : BL_F32, acc, st, dev);
+    const int k_blocks = (int)((K + 127) / 128);
     a.n_tiles = (int)((N + a.rows - 1) / a.rows);
     a.a_pitch = (a.rows + 7) / 8 * 1024;
     const size_t limit = (size_t)dev.max_smem_optin;
@@ -1218,7 +1242,6 @@ bl_status run_linear_int8_few(const int8_t* Xq, const float* sx, int64_t T, int6
 
 // |Xq|, |Wq| <= 128: a sum of K products stays below 2^31 for K < 2^17.
 constexpr int64_t kMaxInt8K = int64_t(1) << 17;
-constexpr int64_t kFewTokens = 192;
 
 }  // namespace
 
@@ -1899,15 +1922,8 @@ bl_status bitlinear_linear_int8(const int8_t* Xq, const float* sx, int64_t T, in
     DeviceInfo dev;
     BL_TRY(current_device(&dev));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // The few-token kernel up to 192 tokens, and up to one token tile (256) while the large tiles of
-    // 256 weight rows would fill less than half the pairs (256 tokens: 4096 x 4096 15.3 us against
-    // 21.6, 28672 x 8192 65.2 against 57.6)
-    if (T <= kFewTokens || (T <= bl::kI8MaxTokens && (N + 255) / 256 * 4 < dev.sms)) {
-        if (y_dt == BL_BF16)
-            return run_linear_int8_few<true>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
-        return run_linear_int8_few<false>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
-    }
-    return run_linear_rows<true>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, y_dt, acc, st, dev);
+    if (y_dt == BL_BF16) return run_linear_int8<true>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
+    return run_linear_int8<false>(Xq, sx, T, K, Wq_i8, gamma_rows, N, Y, acc, st, dev);
 }
 
 bl_status bl_mma_peak_probe(int kind, int pair, int iters, double* ops_out, void* stream) {

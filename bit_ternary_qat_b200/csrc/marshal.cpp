@@ -27,12 +27,13 @@ decltype(&bitlinear_grad_norm) p_grad_norm;
 decltype(&bitlinear_clip_grads) p_clip_grads;
 decltype(&bitlinear_quant_weight_int8) p_quant_weight_int8;
 decltype(&bitlinear_linear_int8) p_linear_int8;
+decltype(&bitlinear_optimizer_step_coef) p_optimizer_step_coef;
 PyObject* g_raise = nullptr;   // raises the binding's error for (entry point, status)
 
 // Interned names of the result dictionaries' keys.
 struct Keys {
     PyObject *x, *h, *xq, *sx, *xdq, *r_post, *r_pre, *dx, *dy, *dpost_gain, *dpre_gain, *dgate, *norm, *coef, *grads,
-        *gamma_rows, *wq_i8, *wq_bf16;
+        *gamma_rows, *gamma, *wq_i8, *wq_bf16, *packed;
 } K;
 
 // Owned reference to a dictionary under construction.
@@ -326,6 +327,46 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (W, dW, m, v, step, lr, beta1, beta2, eps, weight_decay, requantize, ws, out, coef)
+PyObject* optimizer_step_coef(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    nargs_are(n, 14);
+    const at::Tensor& W = tensor(a[0], "W");
+    TORCH_CHECK_VALUE(W.is_cuda() && W.dim() == 2, "W must be a CUDA tensor [N, K]");
+    const at::Device dev = W.device();
+    const int64_t N = W.size(0), Kd = W.size(1);
+    const int64_t shape[2] = {N, Kd}, one[1] = {1}, packed[2] = {N, Kd / 4};
+    auto* w = static_cast<float*>(address(W, "W", at::kFloat, shape, dev));
+    auto* g = static_cast<const float*>(address(tensor(a[1], "dW"), "dW", at::kFloat, shape, dev));
+    auto* m = static_cast<float*>(address(tensor(a[2], "m"), "m", at::kFloat, shape, dev));
+    auto* v = static_cast<float*>(address(tensor(a[3], "v"), "v", at::kFloat, shape, dev));
+    auto* step = static_cast<int32_t*>(address(tensor(a[4], "step"), "step", at::kInt, one, dev));
+    auto* coef = static_cast<const float*>(address(tensor(a[13], "coef"), "coef", at::kFloat, one, dev));
+    float hp[5];
+    for (int i = 0; i < 5; ++i) hp[i] = (float)number(a[5 + i]);
+    const On on(dev);
+    Dict o(a[12]);
+    const bool next = truth(a[10]);
+    auto want = [&](PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef sh) -> void* {
+        return next || PyDict_Contains(o.d, key) == 1 ? output(o, key, name, type, sh, dev) : nullptr;
+    };
+    auto* gamma = static_cast<float*>(want(K.gamma, "gamma", at::kFloat, one));
+    auto* q = static_cast<int8_t*>(want(K.wq_i8, "wq_i8", at::kChar, shape));
+    auto* b = static_cast<uint16_t*>(want(K.wq_bf16, "wq_bf16", at::kBFloat16, shape));
+    auto* p = static_cast<uint8_t*>(want(K.packed, "packed", at::kByte, packed));
+    at::Tensor own;
+    size_t ws_bytes = 0;
+    void* ws = workspace(a[11], p_workspace_bytes(1, N, 1), dev, &own, &ws_bytes);
+    if (failed(unlocked([&] {
+                   return p_optimizer_step_coef(w, g, m, v, N, Kd, hp[0], hp[1], hp[2], hp[3], hp[4], coef, step, q, b,
+                                                p, gamma, ws, ws_bytes, on.stream);
+               }),
+               "bitlinear_optimizer_step_coef"))
+        return nullptr;
+    return o.release();
+    END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------------------------------
 // 8-bit linear
 // ------------------------------------------------------------------------------------
@@ -403,9 +444,9 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // (addresses of the entry points in the order below, raise)
 PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    nargs_are(n, 8);
-    void* p[7];
-    for (int i = 0; i < 7; ++i) {
+    nargs_are(n, 9);
+    void* p[8];
+    for (int i = 0; i < 8; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (p[i] == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null entry point");
@@ -419,9 +460,10 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p_clip_grads = reinterpret_cast<decltype(p_clip_grads)>(p[4]);
     p_quant_weight_int8 = reinterpret_cast<decltype(p_quant_weight_int8)>(p[5]);
     p_linear_int8 = reinterpret_cast<decltype(p_linear_int8)>(p[6]);
-    Py_INCREF(a[7]);
+    p_optimizer_step_coef = reinterpret_cast<decltype(p_optimizer_step_coef)>(p[7]);
+    Py_INCREF(a[8]);
     Py_XDECREF(g_raise);
-    g_raise = a[7];
+    g_raise = a[8];
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -429,7 +471,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define BL_METHOD(f) \
     { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {BL_METHOD(init), BL_METHOD(residual_norm), BL_METHOD(residual_norm_backward), BL_METHOD(grads),
-                         BL_METHOD(quant_weight_int8), BL_METHOD(linear_int8), {nullptr, nullptr, 0, nullptr}};
+                         BL_METHOD(quant_weight_int8), BL_METHOD(linear_int8),
+                         BL_METHOD(optimizer_step_coef), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -441,7 +484,8 @@ PyMODINIT_FUNC PyInit__marshal() {
     } keys[] = {{&K.x, "x"}, {&K.h, "h"}, {&K.xq, "xq"}, {&K.sx, "sx"}, {&K.xdq, "xdq"}, {&K.r_post, "r_post"},
                 {&K.r_pre, "r_pre"}, {&K.dx, "dx"}, {&K.dy, "dy"}, {&K.dpost_gain, "dpost_gain"},
                 {&K.dpre_gain, "dpre_gain"}, {&K.dgate, "dgate"}, {&K.norm, "norm"}, {&K.coef, "coef"},
-                {&K.grads, "grads"}, {&K.gamma_rows, "gamma_rows"}, {&K.wq_i8, "wq_i8"}, {&K.wq_bf16, "wq_bf16"}};
+                {&K.grads, "grads"}, {&K.gamma_rows, "gamma_rows"}, {&K.wq_i8, "wq_i8"}, {&K.wq_bf16, "wq_bf16"}, {&K.gamma, "gamma"},
+                {&K.packed, "packed"}};
     for (auto& k : keys) {
         *k.at = PyUnicode_InternFromString(k.name);
         if (*k.at == nullptr) return nullptr;

@@ -42,18 +42,11 @@ def _stream(device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _same(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
-    """Address of a contiguous tensor of this type, shape and device; raises if it is another."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
-                     f"{tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (not contiguous)"))
-
-
 # The C++ part of this binding: the calls whose kernels run for a few microseconds.
 _marshal_module = None
 _MARSHALLED = ("bitlinear_workspace_bytes", "bitlinear_residual_norm", "bitlinear_residual_norm_backward",
-               "bitlinear_grad_norm", "bitlinear_clip_grads", "bitlinear_quant_weight_int8", "bitlinear_linear_int8")
+               "bitlinear_grad_norm", "bitlinear_clip_grads", "bitlinear_quant_weight_int8", "bitlinear_linear_int8",
+               "bitlinear_optimizer_step_coef")
 
 
 def _raise(name: str, status: int):
@@ -69,19 +62,6 @@ def _marshal():
         module.init(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _MARSHALLED), _raise)
         _marshal_module = module
     return _marshal_module
-
-
-_raw_stream = torch._C._cuda_getCurrentRawStream    # current_stream().cuda_stream without the Stream object
-
-
-def _call(dev, name: str, *args) -> None:
-    """Call an entry point on the current stream of the tensors' device, that device current."""
-    i = dev.index
-    if torch.cuda.current_device() == i:
-        _lib.call(name, *args, _raw_stream(i))
-    else:
-        with torch.cuda.device(dev):
-            _lib.call(name, *args, _raw_stream(i))
 
 
 def workspace_bytes(T: int, N: int, K: int) -> int:
@@ -465,6 +445,9 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
     dict(gamma, wq_i8, wq_bf16, packed) of the updated W (keys from ``out`` are reused).
     coef (fp32 [1], bitlinear_grad_norm's) takes the place of the per-matrix clip: dW is scaled
     by it and max_norm is not used."""
+    if coef is not None:
+        return _marshal().optimizer_step_coef(W, dW, m, v, step, lr, betas[0], betas[1], eps, weight_decay, requantize,
+                                              ws, out, coef)
     for t, name in ((W, "W"), (dW, "dW"), (m, "m"), (v, "v")):
         _cuda(t, name, torch.float32)
     _cuda(step, "step", torch.int32)
@@ -478,16 +461,6 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
         o.setdefault("packed", torch.empty(N, K // 4, dtype=torch.uint8, device=dev))
     if ws is None:
         ws = workspace(1, N, K, dev)
-    if coef is not None:
-        _same(dW, "dW", torch.float32, W.shape, dev)
-        _same(m, "m", torch.float32, W.shape, dev)
-        _same(v, "v", torch.float32, W.shape, dev)
-        _same(step, "step", torch.int32, (1,), dev)
-        _same(coef, "coef", torch.float32, (1,), dev)
-        _call(dev, "bitlinear_optimizer_step_coef", W.data_ptr(), dW.data_ptr(), m.data_ptr(), v.data_ptr(), N, K,
-              lr, betas[0], betas[1], eps, weight_decay, coef.data_ptr(), step.data_ptr(), _ptr(o.get("wq_i8")),
-              _ptr(o.get("wq_bf16")), _ptr(o.get("packed")), _ptr(o.get("gamma")), ws.data_ptr(), ws.numel())
-        return o
     _lib.call("bitlinear_optimizer_step", W.data_ptr(), dW.data_ptr(), m.data_ptr(), v.data_ptr(), N, K,
               float(lr), float(betas[0]), float(betas[1]), float(eps), float(weight_decay), float(max_norm),
               step.data_ptr(), _ptr(o.get("wq_i8")), _ptr(o.get("wq_bf16")), _ptr(o.get("packed")),
