@@ -824,8 +824,9 @@ bl_status run_grads_t(const void* const* grads, void* const* out, const int64_t*
     i = 0;
     do {
         i = gc_fill(tab, grads, out, numel, dtypes, i, count, chunk);
-        pdl_launch(bl::grad_scale_kernel<kMax>, dim3((unsigned)blocks), dim3(bl::kGcThreads), 0, st, tab,
-                   static_cast<const double*>(partials), blocks, max_norm, norm, coef);
+        pdl_launch(chunk >= bl::kGcWide ? bl::grad_scale_kernel<kMax, true> : bl::grad_scale_kernel<kMax, false>,
+                   dim3((unsigned)blocks), dim3(bl::kGcThreads), 0, st, tab, static_cast<const double*>(partials), blocks,
+                   max_norm, norm, coef);
         BL_TRY(launched("grad_scale"));
     } while (i < count);
     return BL_OK;
