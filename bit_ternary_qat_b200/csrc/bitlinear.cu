@@ -956,23 +956,17 @@ bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const De
         return launched("residual_norm");
     }
     if (ring) {
-        // Elements per thread: 32 amortise a row's reductions and scalars best (16384 x 4096 bf16:
-        // 108 us against 126 with 16), but an fp32 residual beside a bf16 block wants the
-        // registers for more groups with two stages (137 against 161 us).
-        constexpr bool kMixed = kBf16X != kBf16Y;
+        // 32 elements a thread amortise a row's reductions and scalars (16384 x 4096, bf16: 117 us
+        // against 126 with 16).  Six groups of 128 threads, but four where an fp32 residual stands
+        // beside a bf16 block: their rows then have two stages (144 us against 159; bf16 alone, four
+        // groups: 122 against 117).
+        constexpr int kCap = kBf16X != kBf16Y ? 512 : 768;
         if (nvec <= 32) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 8>(a, st, dev);
         if (nvec <= 64) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 16>(a, st, dev);
-        if constexpr (kMixed) {
-            if (nvec <= 128) return launch_residual_norm_ring<kBf16X, kBf16Y, 64, 768, 16>(a, st, dev);
-            if (nvec <= 256) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, 768, 16>(a, st, dev);
-            if (nvec <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 256, 768, 16>(a, st, dev);
-            if (nvec <= 1024) return launch_residual_norm_ring<kBf16X, kBf16Y, 512, 1024, 16>(a, st, dev);
-        } else {
-            if (nvec <= 128) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 32>(a, st, dev);
-            if (nvec <= 256) return launch_residual_norm_ring<kBf16X, kBf16Y, 64, 768, 32>(a, st, dev);
-            if (nvec <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, 768, 32>(a, st, dev);
-            if (nvec <= 1024) return launch_residual_norm_ring<kBf16X, kBf16Y, 256, 768, 32>(a, st, dev);
-        }
+        if (nvec <= 128) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, kCap, 32>(a, st, dev);
+        if (nvec <= 256) return launch_residual_norm_ring<kBf16X, kBf16Y, 64, kCap, 32>(a, st, dev);
+        if (nvec <= 512) return launch_residual_norm_ring<kBf16X, kBf16Y, 128, kCap, 32>(a, st, dev);
+        if (nvec <= 1024) return launch_residual_norm_ring<kBf16X, kBf16Y, 256, kCap, 32>(a, st, dev);
         // Longer rows: the gains in shared memory if a row fits beside them (4096 x 11008, 100 us
         // against 139 from global memory), two rows at once if two fit (100 against 113 us)
         const size_t row = rn_fwd_row<kBf16X, kBf16Y>(a), gains = rn_gain_bytes(a.K);
