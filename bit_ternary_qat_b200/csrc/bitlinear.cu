@@ -1157,7 +1157,7 @@ bl_status launch_int8_few(const CUtensorMap& tw, const CUtensorMap& tx, const bl
 // Tiles and K split of the few-token kernel, and their cost: the least time on the busiest SM, in rows
 // of 128 bytes: of each k-block the weight rows and the tokens, and kStep for issuing it (0.08 us); a
 // split pays for its join (two cluster barriers and the way through distributed shared memory, 1 us)
-// and for the partial sums' own bytes.  One token: 4096 x 4096 7.2 us split in 4 (116 rows), 7.6 whole
+// and for the partial sums' own bytes.  One token: 4096 x 4096 7.2 us split in 4 (128 rows), 7.6 whole
 // (28 rows); 11008 x 4096 20.0 split in 4, 10.7 whole (75 rows).
 template <bool kBf16Out>
 bl_status i8_plan(bl::I8Args& a, int64_t* cost_out, int dev_id, const DeviceInfo& dev) {

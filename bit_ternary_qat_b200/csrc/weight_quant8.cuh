@@ -6,7 +6,8 @@
 //   m_n = max(max_k |W[n,k]|, 1e-5),  s_n = fl(127 / m_n),  gamma_n = fl(m_n / 127)
 //   W_q[n,k] = rint(fl(W[n,k] s_n))   in [-127, 127]
 // and the backward's operand W_q * bf16(gamma_n) in bf16.  A row is read twice, the second time
-// out of L1 / L2; HBM-bound on one read of W and the outputs.
+// out of L1 / L2; HBM-bound on one read of W and the outputs (11008 x 4096: 48.4 us for 316 MB, 6.5 TB/s;
+// rows of 32768 leave L1 between the reads: 4096 x 32768 217 us for 940 MB).
 #pragma once
 #include "common.cuh"
 #include "act_quant.cuh"

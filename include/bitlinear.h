@@ -382,7 +382,10 @@ BL_API bl_status bitlinear_optimizer_step_coef(float* W, const float* dW, float*
  * gradients are not refused: an infinite norm gives coef = 0, a NaN one NaN, and norm says so.
  * The same gradients give the same bits on every call and rank, so ranks that hold the same
  * (all-reduced) gradients take the same step.
- * ws: at least bitlinear_workspace_bytes(1, 1, 1) bytes, no initialisation needed.
+ * A NaN or infinite coefficient handed on to bitlinear_optimizer_step_coef spoils the weights:
+ * look at norm first where gradients may not be finite.
+ * ws: at least bitlinear_workspace_bytes(1, 1, 1) bytes, no initialisation needed; calls (or
+ * replayed graphs) that share one must not overlap.
  * Two launches for up to 64 non-empty gradients, two more for each further 960. */
 BL_API bl_status bitlinear_grad_norm(const void* const* grads, const int64_t* numel, const bl_dtype* dtypes,
                               int64_t count, float max_norm, float* norm, float* coef,
@@ -426,8 +429,9 @@ BL_API bl_status bitlinear_residual_norm(const void* X, bl_dtype x_dt, const voi
  * be dXout or dH); dY [T x K] of y_dt (the operand of the block's own backward).  Optional: dg_post,
  * dg_pre fp32 [K]; dgate, shaped and typed as the gate.  ws: at least
  * bitlinear_workspace_bytes(T, 16, K) bytes when dg_post, dg_pre or the gradient of a scalar or
- * channel gate is asked for.  Column sums are fp32 in each of at most 148 blocks and joined in
- * block order: repeatable.  One launch, or two with column sums. */
+ * channel gate is asked for; calls (or replayed graphs) that share one must not overlap.  Column
+ * sums are fp32 in each of at most 148 blocks and joined in block order: repeatable.  One launch,
+ * or two with column sums. */
 BL_API bl_status bitlinear_residual_norm_backward(const float* dXout, const float* dH, const void* Xout,
                                            bl_dtype x_dt, const void* Y, bl_dtype y_dt, int64_t T, int64_t K,
                                            int post_norm, const float* g_post, const float* r_post,
