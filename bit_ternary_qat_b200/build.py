@@ -63,7 +63,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
            *[a for d in cpp_extension.include_paths() for a in ("-isystem", d)],
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
            "-isystem", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp,
-           "-L", lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+           "-L", lib, "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)

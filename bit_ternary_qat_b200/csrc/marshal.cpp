@@ -10,6 +10,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -62,6 +63,11 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
     return THPVariable_Unpack(o);
 }
 
+// A new contiguous tensor, from the caching allocator without the dispatcher (0.5 us less a tensor).
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
+    return at::detail::empty_cuda(shape, type, dev, std::nullopt);
+}
+
 // The address of a contiguous tensor of this type, shape and device.
 void* address(const at::Tensor& t, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev) {
     TORCH_CHECK_VALUE(t.scalar_type() == type && t.sizes() == shape && t.device() == dev && t.is_contiguous(), name,
@@ -77,7 +83,7 @@ void* optional(PyObject* o, const char* name, at::ScalarType type, at::IntArrayR
 void* output(Dict& d, PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev) {
     if (PyObject* have = PyDict_GetItemWithError(d.d, key)) return address(tensor(have, name), name, type, shape, dev);
     if (PyErr_Occurred()) throw python_error();
-    const at::Tensor t = at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    const at::Tensor t = fresh(shape, type, dev);
     d.set(key, t);
     return t.data_ptr();
 }
@@ -125,7 +131,7 @@ bool failed(bl_status st, const char* name) {
 // A caller's workspace, or a new one of `bytes`.
 void* workspace(PyObject* ws, size_t bytes, at::Device dev, at::Tensor* own, size_t* size) {
     if (ws == Py_None) {
-        *own = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+        *own = fresh({(int64_t)bytes}, at::kByte, dev);
         *size = bytes;
         return own->data_ptr();
     }
@@ -415,13 +421,13 @@ PyObject* linear_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(THPDtype_Check(a[4]), "out_dtype must be a torch.dtype");
         const at::ScalarType t = reinterpret_cast<THPDtype*>(a[4])->scalar_type;
         type_code(t);
-        y = at::empty({T, N}, at::TensorOptions().dtype(t).device(dev));
+        y = fresh({T, N}, t, dev);
     }
     if (a[7] != Py_None) {
         acc = tensor(a[7], "acc");
         address(acc, "acc", at::kInt, {T, N}, dev);
     } else if (truth(a[5])) {
-        acc = at::empty({T, N}, at::TensorOptions().dtype(at::kInt).device(dev));
+        acc = fresh({T, N}, at::kInt, dev);
     }
     if (failed(unlocked([&] { return p_linear_int8((const int8_t*)px, (const float*)ps, T, Kd, (const int8_t*)pw, (const float*)pg, N,
                              y.data_ptr(), type_code(y.scalar_type()),
