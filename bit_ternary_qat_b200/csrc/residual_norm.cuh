@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(512, 1)
         const uint8_t *dx_r = row + shift(t, 4), *dh_r = dx_r + o_dh, *x_r = row + o_x + shift(t, xs),
                       *y_r = row + o_y + shift(t, ys);
         const int64_t row0 = t * row_vecs + v0;
-        const float b2 = -r2 * r2 * r2 * c2;      // d = dx + r2 g2 dh + x b2
+        const float b2 = -r2 * (r2 * c2);         // d = dx + r2 g2 dh + u2 b2 (r2^3 may leave fp32)
         float wd[VPT][E], u1[VPT][E];
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -889,7 +889,7 @@ __global__ void __launch_bounds__(512, 1)
                 rn_lds<kBf16X, E>(x_r, v, x);
                 rn_gain<true, E>(g2_sm, v, nvec, g2);
 #pragma unroll
-                for (int e = 0; e < E; ++e) d[e] = fmaf(x[e], b2, fmaf(g2[e] * dh[e], r2, d[e]));
+                for (int e = 0; e < E; ++e) d[e] = fmaf(x[e] * r2, b2, fmaf(g2[e] * dh[e], r2, d[e]));
             }
             rn_lds<kBf16Y, E>(y_r, v, u1[j]);
             rn_gain<true, E>(w_sm, v, nvec, w);

@@ -161,6 +161,30 @@ def test_backward_against_differences(bl, gate):
         assert abs(float(along.sum()) - diff) <= 1e-4 * float(along.abs().sum()) + 1e-6, name
 
 
+@pytest.mark.parametrize("T,K", [(6, 1024), (5, 1003), (3, 9216)])
+def test_backward_of_large_and_small_rows(bl, T, K):
+    """Rows far from 1: the statistic's cube leaves fp32 (1e-60, 1e9), the gradient does not."""
+    s = ref.inputs(T, K, F, F, "channel", 15, DEV)
+    for i, f in enumerate([1e20, 1e-4, 1.0][:T]):
+        s["x"][i] *= f
+        s["y"][i] *= f
+    o = bl.bitlinear_residual_norm(**s, mode="norm")
+    gen = torch.Generator().manual_seed(T)
+    dh = torch.randn(T, K, generator=gen).to(DEV)
+    for row in range(T):                                  # a row alone: column sums of one scale
+        one = dict(s, x=s["x"][row:row + 1].clone(), y=s["y"][row:row + 1].clone())
+        o1 = bl.bitlinear_residual_norm(**one, mode="norm")
+        d1 = dh[row:row + 1].clone()
+        got = run_backward(bl, one, o1, None, d1, 1.0, 1.0, True)
+        torch.cuda.synchronize()
+        want = ref.backward(None, d1, o1["x"], one["y"], o1["r_post"], o1["r_pre"], s["g_post"], s["g_pre"], s["gate"],
+                            1.0, 1.0, F)
+        for k, (v, b) in want.items():
+            close(got[k], v, b, f"{k} of row {row}")
+    assert torch.equal(o["x"][0:1], bl.bitlinear_residual_norm(**dict(s, x=s["x"][:1].clone(), y=s["y"][:1].clone()),
+                                                              mode="norm")["x"])
+
+
 def test_in_place(bl):
     """The new residual over the old one, and the gradient over either incoming one."""
     for (T, K), (xt, yt) in [((33, 1184), t) for t in TYPES] + [((1400, 1184), t) for t in TYPES]:
