@@ -413,9 +413,9 @@ __device__ __forceinline__ void rn_gain_put(float* g, int v, int nvec, const flo
         reinterpret_cast<float4*>(g)[i * nvec + v] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
 }
 
-// HBM-bound in bursts, issue-bound at the clock a sustained load leaves (16384 x 4096, fp32 residual
-// beside a bf16 block, quantised: 137 and 151 us for 872 MB; bf16 alone 108 and 117 us for 604 MB; a
-// block per row with direct loads took 241 us).
+// HBM-bound in bursts, issue-bound at the clock a sustained load leaves: 16384 x 4096, fp32 residual
+// beside a bf16 block, quantised, 872 MB in 143 us, up to 152 as the clock falls; bf16 alone, 604 MB,
+// 108 to 117 us.  A block per row with direct loads took 241 us.
 // Forward: thread i of a group owns vectors i + j * TG of E elements, EPT elements in all (kOdd: the
 // rows are no whole 16-byte vectors, E = 1).  kSm:
 // the weights w (for a gate that is the same in every row) and g2 are formed once per block in
