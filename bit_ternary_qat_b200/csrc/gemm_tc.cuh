@@ -585,6 +585,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             for (int c0 = 0; c0 < ucols; c0 += kChunkCols) {
                 const int col0 = col_base + c0;
                 if (col0 >= args.N) break;                     // warp-uniform
+                // gamma_n of the chunk, on its way while the accumulators are read (the same 16 bytes for
+                // every lane; N is a multiple of 16, so a vector is in or out whole)
+                float gn[epi_is_int8(kEpi) ? kChunkCols : 1];
+                if constexpr (epi_is_int8(kEpi)) {
+#pragma unroll
+                    for (int j = 0; j < kChunkCols / 4; ++j) {
+                        const int c = col0 + 4 * j < args.N ? col0 + 4 * j : 0;
+                        const float4 q = __ldg(reinterpret_cast<const float4*>(args.gamma + c));
+                        gn[4 * j] = q.x; gn[4 * j + 1] = q.y; gn[4 * j + 2] = q.z; gn[4 * j + 3] = q.w;
+                    }
+                }
                 uint32_t ra[32], rb[32];
                 __syncwarp();
                 tmem_ld_32x32b_x32(t_row + c0, ra);
@@ -608,18 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                         return cs;
                     }
                 };
-                // the accumulators as fp32, times gamma_n where the epilogue multiplies by it first (the
-                // same 16 bytes for every lane; N is a multiple of 16, so a vector is in or out whole)
+                // the accumulators as fp32, times gamma_n where the epilogue multiplies by it first
                 auto val = [&](int i) -> float { return static_cast<float>(static_cast<int32_t>(r(i))); };
-                float gn[epi_is_int8(kEpi) ? kChunkCols : 1];
-                if constexpr (epi_is_int8(kEpi)) {
-#pragma unroll
-                    for (int j = 0; j < kChunkCols / 4; ++j) {
-                        const int c = col0 + 4 * j < args.N ? col0 + 4 * j : 0;
-                        const float4 q = __ldg(reinterpret_cast<const float4*>(args.gamma + c));
-                        gn[4 * j] = q.x; gn[4 * j + 1] = q.y; gn[4 * j + 2] = q.z; gn[4 * j + 3] = q.w;
-                    }
-                }
                 auto scaled = [&](int i) -> float {
                     if constexpr (epi_is_int8(kEpi)) return __fmul_rn(__fmul_rn(val(i), gn[i]), fac(i));
                     else return __fmul_rn(val(i), fac(i));
