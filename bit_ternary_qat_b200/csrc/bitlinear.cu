@@ -1189,13 +1189,14 @@ bl_status i8_plan(bl::I8Args& a, int64_t* cost_out, int dev_id, const DeviceInfo
     return BL_OK;
 }
 
-// Whether the few-token kernel takes T tokens: always up to 192; beyond that while the large tiles
-// (256 tokens x 256 weight rows on a pair of SMs) fill less than half the pairs and its estimate is
-// lower (us; 256 tokens: 4096 x 4096 15.3 against 21.6, 11008 x 4096 21.3 against 18.8).
-bool i8_few(const bl::I8Args& a, int64_t cost, const DeviceInfo& dev) {
+// Whether the large tiles (256 tokens x 256 weight rows on a pair of SMs) take T tokens: never up to
+// 192, always when they fill half the pairs (256 tokens: 11008 x 4096 18.8 us against 21.3), else when
+// the estimates (us) say so (256 tokens: 4096 x 4096 21.6 against 15.3).
+bool i8_large(int64_t T, int64_t N, const DeviceInfo& dev) {
+    return T > 192 && ((T + 255) / 256) * ((N + 255) / 256) * 4 >= dev.sms;
+}
+bool i8_few(const bl::I8Args& a, int64_t cost) {
     if (a.T <= 192) return true;
-    const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256);
-    if (tiles * 4 >= dev.sms) return false;
     const double few = 4.0 + 0.0022 * (double)cost;
     const double large = 8.0 + 0.3 * ((a.K + 127) / 128) + 0.5 * (double)a.N * a.K / 6.5e6;
     return few < large;
@@ -1211,9 +1212,9 @@ bl_status run_linear_int8(const int8_t* Xq, const float* sx, int64_t T, int64_t 
     bl::I8Args a{};
     a.T = (int)T; a.N = (int)N; a.K = (int)K;
     int64_t cost = 0;
-    // from 74 pairs of 256 tokens on the large tiles fill the device by the tokens alone
-    if (T <= 74 * 256) BL_TRY(i8_plan<kBf16Out>(a, &cost, dev_id, dev));
-    if (T > 74 * 256 || !i8_few(a, cost, dev))
+    const bool large = i8_large(T, N, dev);
+    if (!large) BL_TRY(i8_plan<kBf16Out>(a, &cost, dev_id, dev));
+    if (large || !i8_few(a, cost))
         return run_linear_rows<true>(Xq, sx, T, K, Wq, gamma_rows, N, Y, kBf16Out ? BL_BF16 : BL_F32, acc, st, dev);
     const int k_blocks = (int)((K + 127) / 128);
     a.n_tiles = (int)((N + a.rows - 1) / a.rows);

@@ -51,6 +51,14 @@ def test_shapes(bl, N, K):
         check(bl, T, N, K, out_dtype=F if T % 2 else B)
 
 
+@pytest.mark.parametrize("T,N,K", [(519, 720, 12480), (1131, 64, 7072), (2000, 512, 8192), (700, 256, 16384),
+                                   (300, 48, 1024), (5000, 16, 4096), (4097, 32, 32), (1300, 1040, 160)])
+def test_several_token_tiles(bl, T, N, K):
+    """More tokens than one tile, with few weight rows: tiles of both kinds, split and whole."""
+    check(bl, T, N, K, out_dtype=B)
+    check(bl, T, N, K, out_dtype=F)
+
+
 @pytest.mark.parametrize("seed", range(24))
 def test_random_shapes(bl, seed):
     rng = np.random.default_rng(seed)
