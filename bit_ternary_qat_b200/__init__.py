@@ -21,6 +21,8 @@ from .ops import (  # noqa: F401
 
 
 def load():
-    """Load the CUDA library now (raises if it is not built)."""
+    """Load the CUDA library and the binding's C++ part now (raises if either is not built)."""
     from . import _lib
-    return _lib.lib()
+    L = _lib.lib()
+    ops._marshal()
+    return L
