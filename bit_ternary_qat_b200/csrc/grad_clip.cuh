@@ -207,9 +207,12 @@ __device__ __forceinline__ void gc_scale(const void* g, void* out, int64_t i0, i
     auto vec = [&](const uint4& r) { return make_uint4(word(r.x), word(r.y), word(r.z), word(r.w)); };
     int64_t i = threadIdx.x;
     if (kWide && ((reinterpret_cast<uintptr_t>(pv) | reinterpret_cast<uintptr_t>(qv)) & 31) == 0) {
+        // Whole rounds of the block only, the same number for every thread: the loops below give the
+        // vectors to other threads, so they have to start behind one border.
         const int64_t n2 = nv / 2;
-        int64_t j = threadIdx.x;
-        for (; j + 3 * kGcThreads < n2; j += 4 * kGcThreads) {
+        int64_t b = 0;
+        for (; b + 4 * kGcThreads <= n2; b += 4 * kGcThreads) {
+            const int64_t j = b + threadIdx.x;
             GcVec32 r[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) r[u] = gc_ld32(pv + 2 * (j + u * kGcThreads));
@@ -220,7 +223,7 @@ __device__ __forceinline__ void gc_scale(const void* g, void* out, int64_t i0, i
                 gc_st32(qv + 2 * (j + u * kGcThreads), r[u]);
             }
         }
-        i += 2 * (j - threadIdx.x);
+        i += 2 * b;
     }
     for (; i + 3 * kGcThreads < nv; i += 4 * kGcThreads) {
         uint4 r[4];
