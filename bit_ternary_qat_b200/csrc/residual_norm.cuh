@@ -17,6 +17,7 @@
 #pragma once
 #include "common.cuh"
 #include "act_quant.cuh"
+#include "ring_flight.cuh"
 
 namespace bl {
 
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(NT) residual_norm_kernel(const RnFwdArgs a) {
 // barrier (a warp by itself), so the groups' barriers and reductions overlap.  A stage is refilled
 // by the group's first thread once a barrier of the row shows that every thread has read it.
 // Every wait is bounded; after one that ran out the group goes on to its end (with whatever
-// is in shared memory: the status word tells), so that no barrier is left waiting.
+// is in shared memory: the status word tells), so that no barrier is left waiting, but its first
+// thread posts no more copies and at the end waits (with a limit) for those on their way.
 // ------------------------------------------------------------------------------------
 constexpr int kRnMaxStages = 4;
 
@@ -430,11 +432,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     __shared__ uint64_t full[kRG][kRnMaxStages];
     __shared__ double red_y[kRG][2][TG / 32], red_x[kRG][2][TG / 32];
     __shared__ float red_m[kRG][2][TG / 32];
-    __shared__ int abort_flag;
+    __shared__ RingFlight flight[kRG];            // each by its group's first thread alone
+    __shared__ volatile int abort_flag;
     const int g = threadIdx.x / TG, tid = threadIdx.x % TG;
     const int RG = blockDim.x / TG;
     if (threadIdx.x == 0) abort_flag = 0;
     if (tid == 0) {
+        flight[g].reset();
         for (int s = 0; s < stages; ++s) mbar_init(&full[g][s], 1);
         fence_mbar_init();
     }
@@ -576,7 +580,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         if (a.r_pre != nullptr) ss = rn_group_reduce<TG>(ss, red_x[g][par], g, [](double p, double q) { return p + q; });
         if (TG == 32 || a.r_pre == nullptr) rn_group_sync<TG>(g);
         // every thread of the group has read the stage
-        if (tid == 0 && t + stages * step < a.T) issue(t + stages * step, s);
+        if (tid == 0 && t + stages * step < a.T) {
+            if (abort_flag == 0) issue(t + stages * step, s);
+            else flight[g].stop(t);
+        }
         if (++s == stages) { s = 0; ph ^= 1u; }
         if (a.r_pre == nullptr) continue;
 
@@ -614,11 +621,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         }
     }
     if (tid == 0 && abort_flag != 0) {
-        // loads that had not landed when the wait ran out: let them (briefly) before the block ends
-        for (int q = 0; q < stages; ++q) {
-            mbar_wait(&full[g][s], ph, 100000000ull, nullptr);
-            if (++s == stages) { s = 0; ph ^= 1u; }
-        }
+        // loads that had not landed when a wait ran out: let them (briefly) before the block ends
+        flight[g].drain(stages, t_first, step, a.T,
+                        [&](int q, uint32_t parity) { mbar_wait(&full[g][q], parity, 100000000ull, nullptr); });
     }
 }
 
@@ -706,7 +711,8 @@ __global__ void __launch_bounds__(512, 1)
     __shared__ uint64_t xbar[2];
     __shared__ __align__(16) float2 red[kRG][2][kW];
     __shared__ double red_s[kThreads / 32];
-    __shared__ int abort_flag;
+    __shared__ RingFlight flight[kRG];            // each by its group's first thread alone
+    __shared__ volatile int abort_flag;
     const int g = threadIdx.x / TG, tid = threadIdx.x % TG, lane = threadIdx.x & 31;
     const int RG = blockDim.x / TG;
     const int rank = kCl > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -716,6 +722,7 @@ __global__ void __launch_bounds__(512, 1)
         mbar_init(&xbar[1], 1);
     }
     if (tid == 0) {
+        flight[g].reset();
         for (int s = 0; s < stages; ++s) mbar_init(&full[g][s], 1);
         fence_mbar_init();
     }
@@ -801,6 +808,7 @@ __global__ void __launch_bounds__(512, 1)
     const float invK = 1.0f / static_cast<float>(a.K);
 
     uint32_t par = 0, xph = 0;
+    bool apart = false;   // this thread's wait for the cluster ran out: it sends and arms nothing more
     auto reduce = [&](float2 v) -> float2 {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) rn_add2(v, o);
@@ -812,11 +820,14 @@ __global__ void __launch_bounds__(512, 1)
             if (lane == 0) red[g][par][tid >> 5] = v;
             rn_group_sync<TG>(g);
         } else {
-            if (threadIdx.x == 0) mbar_arrive_expect_tx(&xbar[par], kW * 8u);
-            if (lane < kCl)
-                st_async_v2(mapa_shared(smem_u32(&red[0][par][rank * (TG / 32) + (tid >> 5)]), lane),
-                            mapa_shared(smem_u32(&xbar[par]), lane), v);
-            mbar_wait(&xbar[par], xph, wait_ns, &abort_flag);
+            if (!apart) {
+                if (threadIdx.x == 0) mbar_arrive_expect_tx(&xbar[par], kW * 8u);
+                if (lane < kCl)
+                    st_async_v2(mapa_shared(smem_u32(&red[0][par][rank * (TG / 32) + (tid >> 5)]), lane),
+                                mapa_shared(smem_u32(&xbar[par]), lane), v);
+                apart = !mbar_wait(&xbar[par], xph, wait_ns, &abort_flag);
+            }
+            __syncwarp();
         }
         v = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -928,7 +939,10 @@ __global__ void __launch_bounds__(512, 1)
         }
         sum = reduce(sum);
         // every thread of the group has read the stage
-        if (tid == 0 && t + stages * step < a.T) issue(t + stages * step, s_row);
+        if (tid == 0 && t + stages * step < a.T) {
+            if (abort_flag == 0) issue(t + stages * step, s_row);
+            else flight[g].stop(t);
+        }
         r2 = r2n;
         c2 = sum.y * invK;
         if (tid == 0 && rank == 0 && a.gate_kind == kGateToken && a.dgate != nullptr)
@@ -944,14 +958,13 @@ __global__ void __launch_bounds__(512, 1)
         }
     }
     if (tid == 0 && abort_flag != 0) {
-        // loads that had not landed when the wait ran out: let them (briefly) before the block ends
-        for (int q = 0; q < stages; ++q) {
-            mbar_wait(&full[g][s], ph, 100000000ull, nullptr);
-            if (++s == stages) { s = 0; ph ^= 1u; }
-        }
+        // loads that had not landed when a wait ran out: let them (briefly) before the block ends
+        flight[g].drain(stages, t_first, step, a.T,
+                        [&](int q, uint32_t parity) { mbar_wait(&full[g][q], parity, 100000000ull, nullptr); });
     }
     __syncthreads();                              // every group is through its rows and its loads
-    if (a.part_pre != nullptr || a.part_s != nullptr || a.part_scalar != nullptr) {
+    // (a load that never landed may still: nothing is written over the ring then)
+    if (abort_flag == 0 && (a.part_pre != nullptr || a.part_s != nullptr || a.part_scalar != nullptr)) {
         float* sums = reinterpret_cast<float*>(rn_smem);   // [group][2][cols]
         float* mine = sums + static_cast<size_t>(g) * 2 * cols;
 #pragma unroll
