@@ -883,7 +883,7 @@ size_t rn_ws_bytes(int64_t K) {
 template <bool kBf16X, bool kBf16Y, bool kWarpRow, int E, int NT, int VPT>
 void launch_residual_norm_v(const bl::RnFwdArgs& a, cudaStream_t st) {
     constexpr int kRows = kWarpRow ? NT / 32 : 1;
-    const dim3 grid((unsigned)((a.T + kRows - 1) / kRows));
+    const dim3 grid((unsigned)(((int64_t)a.T + kRows - 1) / kRows));
     if (a.gate_kind == bl::kGateElement)
         pdl_launch(bl::residual_norm_kernel<kBf16X, kBf16Y, kWarpRow, E, NT, VPT, true>, grid, dim3(NT), 0, st, a);
     else
@@ -919,7 +919,7 @@ bl_status launch_residual_norm_ring_v(const bl::RnFwdArgs& a, cudaStream_t st, c
         if (e != cudaSuccess) return fail(BL_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         attr_set.fetch_or(1ull << dev_id);
     }
-    const int64_t blocks = std::min<int64_t>((a.T + groups - 1) / groups, dev.sms);
+    const int64_t blocks = std::min<int64_t>(((int64_t)a.T + groups - 1) / groups, dev.sms);
     pdl_launch(kern, dim3((unsigned)blocks), dim3((unsigned)(TG * groups)), smem, st, a, stages, g_wait_ns.load());
     return launched("residual_norm_ring");
 }
@@ -1038,7 +1038,7 @@ bl_status launch_residual_norm_bwd_ring(const bl::RnBwdArgs& a, cudaStream_t st,
         }
         if (dev_id >= 0 && dev_id < 64) slots[dev_id].store(n);
     }
-    *G = (int)std::min<int64_t>((a.T + groups - 1) / groups, std::min(n, (int)bl::kRnMaxBlocks / kCl));
+    *G = (int)std::min<int64_t>(((int64_t)a.T + groups - 1) / groups, std::min(n, (int)bl::kRnMaxBlocks / kCl));
     *Gs = *G * kCl;
     cfg.gridDim = dim3((unsigned)*Gs);
     cfg.dynamicSmemBytes = smem;
