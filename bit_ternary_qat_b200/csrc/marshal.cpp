@@ -266,6 +266,28 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // ------------------------------------------------------------------------------------
 // gradient norm and clipping
 // ------------------------------------------------------------------------------------
+// Bytes that a call reads or writes.  Its blocks run in any order, so what one writes no other may
+// read or write; only a gradient clipped in place is both (by one thread an element).
+struct Span {
+    uintptr_t lo, hi;
+};
+bool by_start(const Span& p, const Span& q) { return p.lo < q.lo; }
+// `written` must not touch one another or `read` (both are sorted here: under a microsecond for 58 tensors).
+bool disjoint(std::vector<Span>& read, std::vector<Span>& written) {
+    std::sort(read.begin(), read.end(), by_start);
+    std::sort(written.begin(), written.end(), by_start);
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].lo < written[i - 1].hi) return false;
+    // what is read may overlap: the furthest end of all that start before the written piece's end
+    size_t r = 0;
+    uintptr_t end = 0;
+    for (const Span& w : written) {
+        for (; r < read.size() && read[r].lo < w.hi; ++r) end = std::max(end, read[r].hi);
+        if (end > w.lo) return false;
+    }
+    return true;
+}
+
 // (clip, grads, max_norm, out, norm, coef, ws)
 PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -288,7 +310,17 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Device dev = tensor(g.at(0), "grads[0]").device();
     TORCH_CHECK_VALUE(dev.is_cuda(), "grads must be CUDA tensors");
     std::vector<const void*> ptrs(count);
-    std::vector<void*> outs(count), written;
+    std::vector<void*> outs(count);
+    // a norm into new tensors writes to nothing that the caller has
+    const bool look = clip || a[4] != Py_None || a[5] != Py_None || a[6] != Py_None;
+    std::vector<Span> read, written;
+    if (look) {
+        read.reserve(count);
+        written.reserve(count + 3);
+    }
+    auto span = [](std::vector<Span>& to, const void* p, size_t bytes) {
+        if (bytes != 0) to.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes});
+    };
     std::vector<int64_t> numel(count);
     std::vector<bl_dtype> types(count);
     for (Py_ssize_t i = 0; i < count; ++i) {
@@ -302,11 +334,10 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ptrs[i] = t.data_ptr();
         outs[i] = u.data_ptr();
         numel[i] = t.numel();
-        if (clip && numel[i] != 0) written.push_back(outs[i]);
+        const size_t bytes = numel[i] * (types[i] == BL_F32 ? 4 : 2);
+        if (clip) span(written, outs[i], bytes);
+        if (look && (!clip || outs[i] != ptrs[i])) span(read, ptrs[i], bytes);
     }
-    std::sort(written.begin(), written.end());
-    TORCH_CHECK_VALUE(std::adjacent_find(written.begin(), written.end()) == written.end(),
-                      "a gradient is written twice");
     const On on(dev);
     Dict o(Py_None);
     const int64_t one[1] = {1};
@@ -317,6 +348,12 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     at::Tensor own;
     size_t ws_bytes = 0;
     void* ws = workspace(a[6], p_workspace_bytes(1, 1, 1), dev, &own, &ws_bytes);
+    if (a[4] != Py_None) span(written, norm, 4);
+    if (a[5] != Py_None) span(written, coef, 4);
+    if (a[6] != Py_None) span(written, ws, ws_bytes);
+    if (look)
+        TORCH_CHECK_VALUE(disjoint(read, written), "outputs (norm, coef, out, the workspace) must not overlap one another or a "
+                                                   "gradient; only out[i] may be grads[i] itself");
     const float max_norm = (float)number(a[2]);
     if (clip) {
         if (failed(unlocked([&] { return p_clip_grads(ptrs.data(), outs.data(), numel.data(), types.data(), count, max_norm, norm, coef, ws,

@@ -482,7 +482,8 @@ def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tenso
 def bitlinear_clip_grads(grads, max_norm: float = 1.0, out=None, norm: Optional[torch.Tensor] = None,
                          coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
     """Scales a list of gradients by the clip coefficient of their global norm, in place or into
-    ``out``.  Returns dict(norm [1] f32, coef [1] f32, grads: the scaled list)."""
+    ``out``.  out[i] may be grads[i]; what is written overlaps nothing else (refused).
+    Returns dict(norm [1] f32, coef [1] f32, grads: the scaled list)."""
     return _marshal().grads(True, grads, max_norm, out, norm, coef, ws)
 
 
