@@ -303,7 +303,8 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
         PyObject* at(Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(s, i); }
     };
     const Seq g(a[1], "grads must be a sequence of tensors");
-    const Seq q(a[3] == Py_None ? a[1] : a[3], "out must be a sequence of tensors");
+    // in place: the same list (an iterator is used up by the first)
+    const Seq q(a[3] == Py_None ? g.s : a[3], "out must be a sequence of tensors");
     const Py_ssize_t count = g.size();
     TORCH_CHECK_VALUE(count > 0, "grads must not be empty");
     TORCH_CHECK_VALUE(q.size() == count, "out must have ", count, " tensors, got ", q.size());
@@ -360,7 +361,7 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 ws_bytes, on.stream); }),
                    "bitlinear_clip_grads"))
             return nullptr;
-        if (PyDict_SetItem(o.d, K.grads, a[3] == Py_None ? a[1] : a[3])) throw python_error();
+        if (PyDict_SetItem(o.d, K.grads, q.s)) throw python_error();
     } else if (failed(unlocked([&] { return p_grad_norm(ptrs.data(), numel.data(), types.data(), count, max_norm, norm, coef, ws, ws_bytes,
                                   on.stream); }),
                       "bitlinear_grad_norm")) {
