@@ -40,8 +40,16 @@ struct Keys {
 // Owned reference to a dictionary under construction.
 struct Dict {
     PyObject* d;
-    explicit Dict(PyObject* out) : d(out == Py_None ? PyDict_New() : PyDict_Copy(out)) {
+    explicit Dict(PyObject* out) : d(PyDict_Check(out) ? PyDict_Copy(out) : PyDict_New()) {
         if (d == nullptr) throw python_error();
+        // as dict(out or {}): nothing, a dict, or another mapping of names
+        if (out == Py_None || PyDict_Check(out)) return;
+        if (!PyMapping_Check(out) || PyDict_Update(d, out) != 0) {
+            Py_CLEAR(d);
+            PyErr_Clear();
+            PyErr_Format(PyExc_TypeError, "out must be a dict of tensors, got %s", Py_TYPE(out)->tp_name);
+            throw python_error();
+        }
     }
     ~Dict() { Py_XDECREF(d); }
     PyObject* release() {
