@@ -37,25 +37,48 @@ struct Keys {
         *gamma_rows, *gamma, *wq_i8, *wq_bf16, *packed;
 } K;
 
-// Owned reference to a dictionary under construction.
+// The result of a call under construction, and the outputs that the caller gave.  The result holds
+// what the call writes and nothing else that the caller's dictionary may hold from another call.
 struct Dict {
-    PyObject* d;
-    explicit Dict(PyObject* out) : d(PyDict_Check(out) ? PyDict_Copy(out) : PyDict_New()) {
-        if (d == nullptr) throw python_error();
-        // as dict(out or {}): nothing, a dict, or another mapping of names
-        if (out == Py_None || PyDict_Check(out)) return;
-        if (!PyMapping_Check(out) || PyDict_Update(d, out) != 0) {
-            Py_CLEAR(d);
-            PyErr_Clear();
-            PyErr_Format(PyExc_TypeError, "out must be a dict of tensors, got %s", Py_TYPE(out)->tp_name);
+    PyObject *d = nullptr, *given = nullptr;
+    explicit Dict(PyObject* out) {
+        if (PyDict_Check(out)) {
+            Py_INCREF(out);
+            given = out;
+        } else if (out != Py_None) {
+            given = PyDict_New();
+            if (given == nullptr) throw python_error();
+            if (!PyMapping_Check(out) || PyDict_Update(given, out) != 0) {
+                Py_CLEAR(given);
+                PyErr_Clear();
+                PyErr_Format(PyExc_TypeError, "out must be a dict of tensors, got %s", Py_TYPE(out)->tp_name);
+                throw python_error();
+            }
+        }
+        d = PyDict_New();
+        if (d == nullptr) {
+            Py_CLEAR(given);
             throw python_error();
         }
     }
-    ~Dict() { Py_XDECREF(d); }
+    Dict(const Dict&) = delete;
+    ~Dict() {
+        Py_XDECREF(d);
+        Py_XDECREF(given);
+    }
     PyObject* release() {
         PyObject* r = d;
         d = nullptr;
         return r;
+    }
+    // The caller's output (a borrowed reference), or nullptr: none, or None.
+    PyObject* find(PyObject* key) const {
+        PyObject* have = given == nullptr ? nullptr : PyDict_GetItemWithError(given, key);
+        if (have == nullptr && PyErr_Occurred()) throw python_error();
+        return have == Py_None ? nullptr : have;
+    }
+    void put(PyObject* key, PyObject* o) {
+        if (PyDict_SetItem(d, key, o)) throw python_error();
     }
     void set(PyObject* key, const at::Tensor& t) {
         PyObject* o = THPVariable_Wrap(t);
@@ -87,13 +110,20 @@ void* optional(PyObject* o, const char* name, at::ScalarType type, at::IntArrayR
     return o == Py_None ? nullptr : address(tensor(o, name), name, type, shape, dev);
 }
 
-// The output `key`: the caller's, checked, or a new one.
-void* output(Dict& d, PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev) {
-    if (PyObject* have = PyDict_GetItemWithError(d.d, key)) return address(tensor(have, name), name, type, shape, dev);
-    if (PyErr_Occurred()) throw python_error();
+// The output `key`: the caller's (`have`), checked, or a new one.
+void* output(Dict& d, PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev,
+             PyObject* have) {
+    if (have != nullptr && have != Py_None) {
+        void* p = address(tensor(have, name), name, type, shape, dev);
+        d.put(key, have);
+        return p;
+    }
     const at::Tensor t = fresh(shape, type, dev);
     d.set(key, t);
     return t.data_ptr();
+}
+void* output(Dict& d, PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef shape, at::Device dev) {
+    return output(d, key, name, type, shape, dev, d.find(key));
 }
 
 double number(PyObject* o) {
@@ -218,7 +248,7 @@ PyObject* residual_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* h = norm ? output(o, K.h, "h", r.yt, shape, r.dev) : nullptr;
     void* xq = quant ? output(o, K.xq, "xq", at::kChar, shape, r.dev) : nullptr;
     void* sx = quant ? output(o, K.sx, "sx", at::kFloat, row, r.dev) : nullptr;
-    void* xdq = quant && want_xdq ? output(o, K.xdq, "xdq", r.yt, shape, r.dev) : nullptr;
+    void* xdq = quant && (want_xdq || o.find(K.xdq) != nullptr) ? output(o, K.xdq, "xdq", r.yt, shape, r.dev) : nullptr;
     if (failed(unlocked([&] { return p_residual_norm(r.px, type_code(r.xt), r.py, type_code(r.yt), r.T, r.N, post ? 1 : 0, g_post, eps_post,
                                r.kind, r.gate, alpha, beta, g_pre, eps_pre, x, (float*)r_post, (float*)r_pre, h,
                                (int8_t*)xq, (float*)sx, xdq, on.stream); }),
@@ -241,17 +271,17 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto* g_post = static_cast<const float*>(optional(a[6], "g_post", at::kFloat, col, r.dev));
     const auto* g_pre = static_cast<const float*>(optional(a[10], "g_pre", at::kFloat, col, r.dev));
     const float alpha = (float)number(a[8]), beta = (float)number(a[9]);
-    const bool gains = truth(a[11]), want_gate = truth(a[12]) && r.gate != nullptr;
+    const bool gains = truth(a[11]), want_gate = truth(a[12]);
     const bool has_post = a[4] != Py_None, has_dh = a[1] != Py_None;
     TORCH_CHECK_VALUE(!has_dh || a[5] != Py_None, "dh needs r_pre");
     const On on(r.dev);
     Dict o(a[14]);
     void* dX = output(o, K.dx, "dx", at::kFloat, shape, r.dev);
     void* dY = output(o, K.dy, "dy", r.yt, shape, r.dev);
-    void* dg_post = gains && has_post ? output(o, K.dpost_gain, "dpost_gain", at::kFloat, col, r.dev) : nullptr;
-    void* dg_pre = gains && has_dh ? output(o, K.dpre_gain, "dpre_gain", at::kFloat, col, r.dev) : nullptr;
+    void* dg_post = has_post && (gains || o.find(K.dpost_gain) != nullptr) ? output(o, K.dpost_gain, "dpost_gain", at::kFloat, col, r.dev) : nullptr;
+    void* dg_pre = has_dh && (gains || o.find(K.dpre_gain) != nullptr) ? output(o, K.dpre_gain, "dpre_gain", at::kFloat, col, r.dev) : nullptr;
     void* dgate = nullptr;
-    if (want_gate) {
+    if (r.gate != nullptr && (want_gate || o.find(K.dgate) != nullptr)) {
         const at::Tensor& g = THPVariable_Unpack(a[7]);
         dgate = output(o, K.dgate, "dgate", g.scalar_type(), g.sizes(), r.dev);
     }
@@ -350,10 +380,8 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const On on(dev);
     Dict o(Py_None);
     const int64_t one[1] = {1};
-    if (a[4] != Py_None && PyDict_SetItem(o.d, K.norm, a[4])) throw python_error();
-    if (a[5] != Py_None && PyDict_SetItem(o.d, K.coef, a[5])) throw python_error();
-    auto* norm = static_cast<float*>(output(o, K.norm, "norm", at::kFloat, one, dev));
-    auto* coef = static_cast<float*>(output(o, K.coef, "coef", at::kFloat, one, dev));
+    auto* norm = static_cast<float*>(output(o, K.norm, "norm", at::kFloat, one, dev, a[4]));
+    auto* coef = static_cast<float*>(output(o, K.coef, "coef", at::kFloat, one, dev, a[5]));
     at::Tensor own;
     size_t ws_bytes = 0;
     void* ws = workspace(a[6], p_workspace_bytes(1, 1, 1), dev, &own, &ws_bytes);
@@ -369,7 +397,7 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                 ws_bytes, on.stream); }),
                    "bitlinear_clip_grads"))
             return nullptr;
-        if (PyDict_SetItem(o.d, K.grads, q.s)) throw python_error();
+        o.put(K.grads, q.s);
     } else if (failed(unlocked([&] { return p_grad_norm(ptrs.data(), numel.data(), types.data(), count, max_norm, norm, coef, ws, ws_bytes,
                                   on.stream); }),
                       "bitlinear_grad_norm")) {
@@ -400,7 +428,7 @@ PyObject* optimizer_step_coef(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Dict o(a[12]);
     const bool next = truth(a[10]);
     auto want = [&](PyObject* key, const char* name, at::ScalarType type, at::IntArrayRef sh) -> void* {
-        return next || PyDict_Contains(o.d, key) == 1 ? output(o, key, name, type, sh, dev) : nullptr;
+        return next || o.find(key) != nullptr ? output(o, key, name, type, sh, dev) : nullptr;
     };
     auto* gamma = static_cast<float*>(want(K.gamma, "gamma", at::kFloat, one));
     auto* q = static_cast<int8_t*>(want(K.wq_i8, "wq_i8", at::kChar, shape));
@@ -434,7 +462,7 @@ PyObject* quant_weight_int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const On on(dev);
     Dict o(a[3]);
     void* gm = output(o, K.gamma_rows, "gamma_rows", at::kFloat, row, dev);
-    auto wanted = [&](PyObject* want, PyObject* key) { return truth(want) || PyDict_Contains(o.d, key) == 1; };
+    auto wanted = [&](PyObject* want, PyObject* key) { return truth(want) || o.find(key) != nullptr; };
     void* q = wanted(a[1], K.wq_i8) ? output(o, K.wq_i8, "wq_i8", at::kChar, shape, dev) : nullptr;
     void* b = wanted(a[2], K.wq_bf16) ? output(o, K.wq_bf16, "wq_bf16", at::kBFloat16, shape, dev) : nullptr;
     if (failed(unlocked([&] { return p_quant_weight_int8((const float*)w, shape[0], shape[1], (int8_t*)q, (uint16_t*)b, (float*)gm, on.stream); }),

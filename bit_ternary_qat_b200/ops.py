@@ -500,7 +500,8 @@ def bitlinear_residual_norm(x: torch.Tensor, y: torch.Tensor, post_norm: bool = 
     the norm of x' quantised (mode "quant": the operand of bitlinear_linear*), as it is ("norm")
     or not taken ("none").  gate: None, [1], [K] or [T, 1] fp32, or [T, K] of y's type.
     Returns dict(x [T,K] of x's type, r_post [T] f32 with post_norm, and by mode: r_pre [T] f32,
-    xq [T,K] i8, sx [T] f32, xdq [T,K] of y's type; or r_pre, h [T,K] of y's type).
+    xq [T,K] i8, sx [T] f32, xdq [T,K] of y's type; or r_pre, h [T,K] of y's type), with the
+    tensors of ``out`` that bear these names (an xdq among them is written also without want_xdq).
     out["x"] may be x itself."""
     return _marshal().residual_norm(x, y, post_norm, g_post, gate, alpha, beta, mode, g_pre, eps_post, eps_pre, want_xdq,
                                     out)
@@ -516,8 +517,8 @@ def bitlinear_residual_norm_backward(dx: Optional[torch.Tensor], dh: Optional[to
     the next block (or None); dh [T,K] f32: gradient of the norm output, bitlinear_grad_input's
     result (or None: mode "none").  x: the forward's NEW residual; r_post (None: no post norm),
     r_pre: its saved statistics.  Returns dict(dx [T,K] f32, dy [T,K] of y's type, and with
-    want_dgains / want_dgate: dpost_gain [K], dpre_gain [K] f32 (with the norm in question),
-    dgate as the gate).  out["dx"] may be dx or dh."""
+    want_dgains / want_dgate, or where ``out`` holds them: dpost_gain [K], dpre_gain [K] f32 (with
+    the norm in question), dgate as the gate).  out["dx"] may be dx or dh."""
     return _marshal().residual_norm_backward(dx, dh, x, y, r_post, r_pre, g_post, gate, alpha, beta, g_pre, want_dgains,
                                              want_dgate, ws, out)
 
