@@ -21,8 +21,7 @@ from .ops import (  # noqa: F401
 
 
 def load():
-    """Load the CUDA library and the binding's C++ part now (raises if either is not built)."""
+    """Load the CUDA library now (raises if it is not built).  The calls whose binding is in C++
+    load that part when they are first used, and raise if it is not built."""
     from . import _lib
-    L = _lib.lib()
-    ops._marshal()
-    return L
+    return _lib.lib()

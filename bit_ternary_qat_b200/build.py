@@ -71,8 +71,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     return MARSHAL
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_marshal(force, verbose)
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
@@ -81,6 +80,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, then the binding's C++ part: where that cannot be built (no torch headers) this
+    raises, with the library in place for the calls that need nothing else."""
+    build_lib(force, verbose)
+    build_marshal(force, verbose)
     return LIB
 
 

@@ -9,11 +9,13 @@ to libbitlinear.so.  Every step of the computation runs in the library's kernels
 from __future__ import annotations
 
 import ctypes
+import os
 from typing import Optional
 
 import torch
 
 from . import _lib
+from . import build as _build
 
 _DT = {torch.float32: _lib.BL_F32, torch.bfloat16: _lib.BL_BF16}
 
@@ -58,6 +60,9 @@ def _marshal():
     global _marshal_module
     if _marshal_module is None:
         L = _lib.lib()
+        if not os.path.exists(_build.MARSHAL):
+            raise ImportError(f"{_build.MARSHAL} is not built; run `python -m bit_ternary_qat_b200.build` "
+                              "(g++ and torch's headers)")
         from . import _marshal as module
         module.init(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _MARSHALLED), _raise)
         _marshal_module = module
