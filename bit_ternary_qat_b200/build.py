@@ -47,10 +47,23 @@ def nvcc() -> str:
     return "nvcc"
 
 
+def _torch_mark() -> bytes:
+    """What a _marshal.so built against the installed torch and Python holds (torch's C++ classes
+    change from release to release)."""
+    import torch
+    return ("bitlinear binding for torch %s, Python %d.%d;" % (torch.__version__, *sys.version_info[:2])).encode()
+
+
+def marshal_fits() -> bool:
+    """Whether _marshal.so was built against the installed torch."""
+    with open(MARSHAL, "rb") as f:
+        return _torch_mark() in f.read()
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """The C++ part of the binding (g++, against the installed torch)."""
     if not force and os.path.exists(MARSHAL) and all(
-            os.path.getmtime(s) <= os.path.getmtime(MARSHAL) for s in (MARSHAL_SRC, HEADER)):
+            os.path.getmtime(s) <= os.path.getmtime(MARSHAL) for s in (MARSHAL_SRC, HEADER)) and marshal_fits():
         return MARSHAL
     import sysconfig
 
@@ -60,6 +73,7 @@ def build_marshal(force: bool = False, verbose: bool = False) -> str:
     tmp = MARSHAL + ".tmp.%d" % os.getpid()
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           '-DBL_TORCH_MARK="%s"' % _torch_mark().decode(),
            *[a for d in cpp_extension.include_paths() for a in ("-isystem", d)],
            "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"),
            "-isystem", sysconfig.get_paths()["include"], MARSHAL_SRC, "-o", tmp,

@@ -570,5 +570,8 @@ PyMODINIT_FUNC PyInit__marshal() {
         *k.at = PyUnicode_InternFromString(k.name);
         if (*k.at == nullptr) return nullptr;
     }
-    return PyModule_Create(&module);
+    PyObject* m = PyModule_Create(&module);
+    // what build.py looks for in the file before it is loaded
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", BL_TORCH_MARK) != 0) Py_CLEAR(m);
+    return m;
 }

@@ -63,6 +63,9 @@ def _marshal():
         if not os.path.exists(_build.MARSHAL):
             raise ImportError(f"{_build.MARSHAL} is not built; run `python -m bit_ternary_qat_b200.build` "
                               "(g++ and torch's headers)")
+        if not _build.marshal_fits():
+            raise ImportError(f"{_build.MARSHAL} was built for another torch or Python; run "
+                              "`python -m bit_ternary_qat_b200.build`")
         from . import _marshal as module
         module.init(*(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in _MARSHALLED), _raise)
         _marshal_module = module

@@ -33,3 +33,21 @@ def test_library_is_built_first(no_marshal, monkeypatch):
     with pytest.raises(RuntimeError, match="no headers"):
         build.build()
     assert order == ["library"]
+
+
+def test_another_torch(monkeypatch):
+    """A C++ part built for another torch is neither loaded nor taken as built."""
+    build.build()
+    assert build.marshal_fits() and ops._marshal().built_for.encode() == build._torch_mark()
+    monkeypatch.setattr(ops, "_marshal_module", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "1.0.0")
+        assert not build.marshal_fits()
+        with pytest.raises(ImportError, match="another torch"):
+            pkg.bitlinear_grad_norm([torch.ones(2)])
+        asked = []
+        m.setattr(build.subprocess, "run", lambda cmd, check: asked.append(cmd))
+        m.setattr(build.os, "replace", lambda a, b: None)
+        build.build_marshal()
+        assert len(asked) == 1 and '-DBL_TORCH_MARK="%s"' % build._torch_mark().decode() in asked[0]
+    assert ops._marshal().built_for.encode() == build._torch_mark()
