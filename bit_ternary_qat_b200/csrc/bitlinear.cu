@@ -788,8 +788,9 @@ int64_t gc_fill(bl::GcTable<kMax>& tab, const void* const* grads, void* const* o
     tab.count = tab.chunks = 0;
     tab.chunk = chunk;
     int64_t i = first;
-    for (; i < count && tab.count < kMax; ++i) {
-        if (numel[i] == 0) continue;
+    for (; i < count; ++i) {
+        if (numel[i] == 0) continue;                   // also behind a full table: they need no launch
+        if (tab.count == kMax) break;
         bl::GcTensor& t = tab.t[tab.count++];
         t.g = grads[i];
         t.out = out != nullptr ? out[i] : nullptr;

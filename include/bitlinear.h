@@ -386,7 +386,8 @@ BL_API bl_status bitlinear_optimizer_step_coef(float* W, const float* dW, float*
  * look at norm first where gradients may not be finite.
  * ws: at least bitlinear_workspace_bytes(1, 1, 1) bytes, no initialisation needed; calls (or
  * replayed graphs) that share one must not overlap.
- * Two launches for up to 64 non-empty gradients, two more for each further 960. */
+ * A launch takes up to 960 non-empty gradients: with n of them (at least one launch's worth) the
+ * clip takes 2 ceil(n / 960) launches, the norm ceil(n / 960) + 1. */
 BL_API bl_status bitlinear_grad_norm(const void* const* grads, const int64_t* numel, const bl_dtype* dtypes,
                               int64_t count, float max_norm, float* norm, float* coef,
                               void* ws, size_t ws_bytes, void* stream);
