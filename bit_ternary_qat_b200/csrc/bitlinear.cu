@@ -937,8 +937,14 @@ bl_status launch_residual_norm_ring(const bl::RnFwdArgs& a, cudaStream_t st, con
 template <bool kBf16X, bool kBf16Y>
 bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const DeviceInfo& dev) {
     const int nvec = a.K / 8;
-    // The ring pays from about a megabyte and a half of elements on (4096 columns: 300 rows 6.3 us
-    // with it, 7.8 without, fp32 beside bf16; 256 columns: 1200 rows 4.3 us, 3.6 without)
+    // The ring pays from about a million and a half elements on.  Where it begins to depends on the
+    // width (us with the ring / without; bf16 alone, then fp32 beside bf16, quantised, inputs beyond L2):
+    //   1.26 M elements: 4915 x 256 7.2 / 6.0, 7.9 / 6.6; 1228 x 1024 8.7 / 5.8, 7.9 / 6.2;
+    //                    307 x 4096 9.1 / 7.2, 8.6 / 9.2; 76 x 16384 9.0 / 9.6, 10.1 / 10.0
+    //   2.5 M:           9830 x 256 10.2 / 9.9, 11.2 / 10.4; 2457 x 1024 10.0 / 9.6, 13.3 / 10.2;
+    //                    614 x 4096 10.3 / 11.4, 14.1 / 13.5; 153 x 16384 14.3 / 17.8, 16.1 / 19.0
+    // Rows that are no whole vectors (bf16, norm output): 1672 x 1003 9.8 / 10.6, 335 x 5001 14.0 / 21.9,
+    // 102 x 16381 16.3 / 21.2, but 25811 x 65 26 / 11 (a warp a row, with a row's copies for 65 elements)
     const bool ring = (int64_t)a.T * a.K >= (3 << 19);
     if (a.K % 8 != 0) {
         if (ring) {
@@ -959,8 +965,10 @@ bl_status launch_residual_norm(const bl::RnFwdArgs& a, cudaStream_t st, const De
     if (ring) {
         // 32 elements a thread amortise a row's reductions and scalars (16384 x 4096, bf16: 117 us
         // against 126 with 16).  Six groups of 128 threads, but four where an fp32 residual stands
-        // beside a bf16 block: their rows then have two stages (144 us against 159; bf16 alone, four
-        // groups: 122 against 117).
+        // beside a bf16 block: their rows then have two stages.  16384 rows, us with up to 768 / 512
+        // threads, fp32 beside bf16: 1024 columns 44.7 / 41.6, 2048 82.7 / 78.3, 4096 162 / 150, 8192
+        // 316 / 271 (5120 the other way: 172 / 206); bf16 alone: 35.6 / 35.2, 62.3 / 64.6, 111 / 122,
+        // 215 / 249; fp32 alone: 53.6 / 53.6, 98 / 103, 196 / 202, 390 / 390.
         constexpr int kCap = kBf16X != kBf16Y ? 512 : 768;
         if (nvec <= 32) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 8>(a, st, dev);
         if (nvec <= 64) return launch_residual_norm_ring<kBf16X, kBf16Y, 32, 768, 16>(a, st, dev);
@@ -1063,8 +1071,10 @@ bl_status launch_residual_norm_bwd_v(const bl::RnBwdArgs& a, cudaStream_t st, co
         if (fits(2, 1)) BL_RN(512, 16, 2, true);
         BL_RN(512, 8, 4, true);
     }
-    // 16 columns a thread amortise a row's reduction best (16384 x 4096 bf16: 186 us against 200
-    // with 8), as long as two stages of all the groups fit (fp32, 16384 x 2048: 131 against 124)
+    // 16 columns a thread amortise a row's reduction best (16384 rows of bf16, us against those with 8:
+    // 384 columns 30.0 / 32.0, 768 47 / 54, 1536 78 / 93, 4096 185 / 204, 5120 244 / 351), as long as two
+    // stages of all the groups fit (fp32, 2048: 131 / 126, 4096: 248 / 241; fp32 beside bf16, 4096:
+    // 242 / 212, but 2048: 106 / 112).  Up to 256 columns 8 leave no lane idle (128: 19.3 / 17.9).
     if (a.K <= 256) BL_RN(32, 8, 1);
     if (a.K <= 512) BL_RN(32, 16, 1);
     if (a.K <= 1024 && fits(1, 8)) BL_RN(64, 16, 1);

@@ -166,7 +166,7 @@ __device__ __forceinline__ void gc_st32(void* p, const GcVec32& r) {
                  "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]), "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
                  : "memory");
 }
-// Elements of a chunk from which the 32-byte loop runs (809 MB of fp32: the clip 395 -> 385 us).  Short
+// Elements of a chunk from which the 32-byte loop runs (809 MB of fp32: the clip 395 -> 388 us).  Short
 // chunks would leave most of their bytes to the 16-byte loop, and the wide kernel's registers keep
 // fewer blocks on an SM (15 MB in 50 tensors: 15.8 -> 17.9 us).
 constexpr int64_t kGcWide = 32768;

@@ -8,8 +8,10 @@
 //   h  = x' r2 g2       r2_t = 1/sqrt(mean_k x'^2 + eps2)     (norm in front of the next block)
 // and h is written as it is, or quantised exactly as act_quant.cuh quantises it, or not at all.
 //
-// Arithmetic of the forward (the same in both kernels, so that the 8-bit codes are reproducible):
-// both sums of squares in fp64; every product and sum of an element in fp32 with one rounding each,
+// Arithmetic of the forward, the same in both kernels: both sums of squares in fp64 (added in another
+// order in each: the sums agree to about 2^-46, so that r, and with it a row's codes, can differ by an
+// fp32 step between them in one row of some millions; one kernel on one row always gives the same);
+// every product and sum of an element in fp32 with one rounding each,
 //   x' = fl( fl(x alpha) + fl( fl(y r1) w ) ),   w = fl( fl(gate beta) g1 )
 // (w is the same for every row unless the gate is a token's or an element's); x' rounded once to
 // the residual's type, and h = fl(fl(x' r2) g2) computed from the rounded x' (what the next layer

@@ -390,6 +390,8 @@ def bitlinear_act_quant_tensor(X: torch.Tensor, apply_rmsnorm: bool = True, g: O
 def bitlinear_linear_rows(xq: torch.Tensor, sx: torch.Tensor, wq_i8: torch.Tensor, gamma_rows: torch.Tensor,
                           out_dtype=torch.bfloat16, want_acc: bool = False, y: Optional[torch.Tensor] = None,
                           acc: Optional[torch.Tensor] = None):
+    """y[t,n] = acc[t,n] * (gamma_rows[n] / sx[t]) from ternary codes.  bitlinear_linear_int8 takes the
+    same operands and is faster for few tokens; its scales are rounded in another order."""
     _cuda(xq, "xq", torch.int8)
     _cuda(wq_i8, "wq_i8", torch.int8)
     T, K = xq.shape
@@ -482,7 +484,7 @@ def bitlinear_optimizer_step(W: torch.Tensor, dW: torch.Tensor, m: torch.Tensor,
 
 def bitlinear_grad_norm(grads, max_norm: float = 1.0, norm: Optional[torch.Tensor] = None,
                         coef: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
-    """Global L2 norm of a list of gradients (fp32 or bf16, any shapes) and its clip coefficient.
+    """Global L2 norm of gradients (an iterable; fp32 or bf16, any shapes) and its clip coefficient.
     Returns dict(norm [1] f32, coef [1] f32); coef goes into bitlinear_optimizer_step."""
     return _marshal().grads(False, grads, max_norm, None, norm, coef, ws)
 

@@ -296,7 +296,12 @@ BL_API bl_status bitlinear_act_quant_tensor(const void* X, bl_dtype x_dt, int64_
 
 /* The int8 x ternary linear with a per-row weight scale (the weight rows are the output
  * columns):  y[t,n] = fl32( (float)acc[t,n] * fl32(gamma_rows[n] / sx[t]) ).
- * Arguments as bitlinear_linear with gamma_rows fp32 [N]. */
+ * Arguments as bitlinear_linear with gamma_rows fp32 [N].
+ * This is bitlinear_linear's rounding, for ternary codes beside a packed copy of them
+ * (ternary_gemv_rows gives the same bits for few tokens).  bitlinear_linear_int8 takes the same
+ * operands, rounds its two scales in another order, checks K against the int32 sums of 8-bit codes,
+ * and reads the weight faster for few tokens (28672 x 8192, one token: 39 us, 71 here): the call
+ * where these bits are not needed. */
 BL_API bl_status bitlinear_linear_rows(const int8_t* Xq, const float* sx, int64_t T, int64_t K,
                                 const int8_t* Wq_i8, const float* gamma_rows, int64_t N,
                                 void* Y, bl_dtype y_dt, int32_t* acc, void* stream);
@@ -457,7 +462,8 @@ BL_API bl_status bitlinear_quant_weight_int8(const float* W, int64_t N, int64_t 
  *   Y[t,n]   = fl32( fl32((float)acc[t,n] * gamma_rows[n]) * fl32(1 / sx[t]) )   rounded to y_dt
  * Xq int8 [T x K], sx fp32 [T] (bitlinear_act_quant's or bitlinear_residual_norm's), Wq_i8 int8
  * [N x K], gamma_rows fp32 [N], Y [T x N] of y_dt, acc int32 [T x N] optional.  K < 2^17 (the
- * int32 sums cannot wrap).  One launch. */
+ * int32 sums cannot wrap).  One launch.  For 8-bit codes, and for ternary codes with a scale for each
+ * row where bitlinear_linear_rows' rounding, acc * (gamma / s), is not asked for. */
 BL_API bl_status bitlinear_linear_int8(const int8_t* Xq, const float* sx, int64_t T, int64_t K,
                                 const int8_t* Wq_i8, const float* gamma_rows, int64_t N,
                                 void* Y, bl_dtype y_dt, int32_t* acc, void* stream);
