@@ -384,10 +384,11 @@ PyObject* grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     auto* coef = static_cast<float*>(output(o, K.coef, "coef", at::kFloat, one, dev, a[5]));
     at::Tensor own;
     size_t ws_bytes = 0;
-    void* ws = workspace(a[6], p_workspace_bytes(1, 1, 1), dev, &own, &ws_bytes);
+    const size_t needed = p_workspace_bytes(1, 1, 1);
+    void* ws = workspace(a[6], needed, dev, &own, &ws_bytes);
     if (a[4] != Py_None) span(written, norm, 4);
     if (a[5] != Py_None) span(written, coef, 4);
-    if (a[6] != Py_None) span(written, ws, ws_bytes);
+    if (a[6] != Py_None) span(written, ws, std::min(ws_bytes, needed));   // no more of it is written
     if (look)
         TORCH_CHECK_VALUE(disjoint(read, written), "outputs (norm, coef, out, the workspace) must not overlap one another or a "
                                                    "gradient; only out[i] may be grads[i] itself");

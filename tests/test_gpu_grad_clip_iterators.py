@@ -8,7 +8,8 @@ DEV = "cuda:0"
 def test_iterator_reaches_the_checks():
     """On the CPU: what is refused is the tensors' device, not a second, used-up list."""
     import bit_ternary_qat_b200 as pkg
-    pkg.load()
+    from bit_ternary_qat_b200 import build
+    build.build()
     for call in (pkg.bitlinear_grad_norm, pkg.bitlinear_clip_grads):
         with pytest.raises(ValueError, match="CUDA"):
             call(torch.ones(3) for _ in range(2))

@@ -53,5 +53,12 @@ def test_neighbours_are_taken(bl, flat):
     for lo, hi, at in ((0, 100, 0), (0, 100, 100), (50, 90, 200)):
         assert torch.equal(other[at:at + hi - lo], src[lo:hi] * o["coef"])
     bl.bitlinear_grad_norm([src[:100], src[50:100]], 1.0, norm=src[500:501])
+    # a buffer that is more than the workspace, with the results and a gradient behind that
+    n = bl.workspace_bytes(1, 1, 1)
+    buf = torch.zeros(n + 4096, dtype=torch.uint8, device=DEV)
+    tail = buf[n:].view(F)
+    tail[:100] = src[:100]
+    o = bl.bitlinear_clip_grads([tail[:100]], 1.0, norm=tail[200:201], coef=tail[201:202], ws=buf)
+    assert torch.equal(tail[:100], src[:100] * o["coef"])
     torch.cuda.synchronize()
     assert bl.check_device_status() == 0
